@@ -287,6 +287,93 @@ int w8a16_linear_asym(const uint16_t *X, const uint8_t *packed, const uint16_t *
                       int64_t N, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * ---- int8 activations (W8A8) ----
+ * The linear with both operands in 8 bits: activations quantized per token
+ * (the LightSeq slides' symmetric formula, one scale per row instead of per
+ * channel), the weight as packed by w8_prepack, exact sums of products in
+ * 32-bit integers:
+ *   Y[m,n] = fp16_rne( s_m s_n sum_k q[m,k] (w[k,n] - z_n) + bias_n )
+ *
+ * w8_quantize_per_token -- codes, scale and code sum of every row of X.
+ *   s_m = fp32(max_k |X[m,k]|) / 127,  q[m,k] = clamp( rne( X[m,k] / s_m ),
+ *   -127, 127 ),  sum_m = sum_k q[m,k]   (IEEE fp32 operations; s_m == 0
+ *   gives q = 0)
+ *   X       [M, K] fp32 or fp16 (x_dtype), rows ldx >= K elements apart
+ *           (ldx times the element size a multiple of 16 bytes if M > 1).
+ *   q       [M, K] int8, rows ldq >= K bytes apart, ldq a multiple of 16.
+ *           Bytes between K and ldq are neither read nor written anywhere.
+ *   scales  [M] fp32;  sums  [M] int32.
+ *   M >= 0 (0 is a no-op), K >= 1 with K % 8 == 0.  Inputs must be finite
+ *   (rows are independent: a row that is not spoils only itself).
+ * Errors: W8_ERR_NULL, W8_ERR_SHAPE, W8_ERR_ALIGN, W8_ERR_DTYPE,
+ *         W8_ERR_ALIAS, W8_ERR_DEVICE, W8_ERR_CUDA.
+ */
+int w8_quantize_per_token(const void *X, int x_dtype, int64_t ldx, int64_t M, int64_t K, int8_t *q, int64_t ldq,
+                          float *scales, int32_t *sums, void *stream);
+
+/*
+ * w8_swiglu_quantize_per_token -- the activation between the two products of
+ * a gated MLP, quantized per token in the same pass: H [M, 2K] fp16 holds the
+ * gate in its first K columns and the up projection in the others (the
+ * ChatGLM2 h-to-4h output: 27392 = 2 x 13696),
+ *   h[m,k] = g / (1 + exp(-g)) * u,  g = H[m,k], u = H[m,K+k]   in fp32,
+ * then codes, scales and sums of h as w8_quantize_per_token.  Rows of H are
+ * ldh >= 2K elements apart.  Other arguments and errors as there.
+ */
+int w8_swiglu_quantize_per_token(const uint16_t *H, int64_t ldh, int64_t M, int64_t K, int8_t *q, int64_t ldq,
+                                 float *scales, int32_t *sums, void *stream);
+
+/*
+ * w8a8_linear -- Y = s_m s_n sum_k q[m,k] (w[k,n] - z_n) + bias_n.
+ *
+ *   q         [M, K] int8 activation codes, rows ldq >= K bytes apart (ldq a
+ *             multiple of 16), with x_scales [M] fp32 and x_sums [M] int32
+ *             (the sum of each row's K codes), as w8_quantize_per_token
+ *             writes them.  Codes made elsewhere may be any int8 values.
+ *   packed    w8_prepack output for the [K, N] weight (symmetric or
+ *             asymmetric codes).
+ *   scales    [N] fp16;  zeros  [N] int8 zero points, or NULL for none;
+ *   bias      [N] fp16 or NULL.
+ *   Y         [M, N] fp16; must not overlap any input.
+ *   M >= 0 (0 is a no-op); K >= 1 with K % 8 == 0 and K <= 65536 (the sums
+ *   stay below 2^31 whatever the codes are); N >= 1 with N % 8 == 0.
+ *   workspace of w8a8_workspace_bytes(M, K, N) bytes: the workspace of
+ *             w8a16_linear, same size, same rules; one buffer serves both.
+ * Results: the integer sum is exact and independent of how the work is split;
+ *   fp32 rounds it, the product with s_m and the fused product with s_n plus
+ *   bias, and fp16 the result: |Y - Y_exact| <= 2^-11 |Y_exact| + 2^-22 (|Y_exact -
+ *   bias| + |Y_exact|) in fp16's normal range.  Bit-identical on every call.
+ * Stream ordering as w8a16_linear.
+ * Errors: W8_ERR_NULL, W8_ERR_SHAPE, W8_ERR_ALIGN, W8_ERR_WORKSPACE,
+ *         W8_ERR_ALIAS, W8_ERR_DEVICE, W8_ERR_CUDA.
+ */
+size_t w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N);
+int w8a8_linear(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums, const uint8_t *packed,
+                const uint16_t *scales, const int8_t *zeros, const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K,
+                int64_t N, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * w8a8_linear_grouped -- w8a8_linear with one weight per group of rows (the
+ * experts of a mixture, the rows sorted by expert): rows [offsets[e],
+ * offsets[e+1]) of q times weight e.
+ *
+ *   offsets   [groups + 1] int32 on the DEVICE, non-decreasing, within
+ *             [0, M]: read when the kernel runs, never by the host.  Empty
+ *             groups are allowed.  Rows of Y before offsets[0] and from
+ *             offsets[groups] on are left as they were.  Offsets outside
+ *             [0, M] are clamped to it and a group that ends before it begins
+ *             is empty; groups that overlap race on Y.
+ *   packed    [groups] w8_prepack outputs, one after another; scales, zeros
+ *             and bias [groups, N].
+ *   1 <= groups <= 1024, M <= 2^24.
+ * Other arguments, results and errors as w8a8_linear.
+ */
+int w8a8_linear_grouped(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums,
+                        const int32_t *offsets, int64_t groups, const uint8_t *packed, const uint16_t *scales,
+                        const int8_t *zeros, const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K, int64_t N,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * w8a16_linear_decode_static -- the decode path of w8a16_linear (M <= 16)
  * without a caller-provided workspace.  The pages have no counterpart: this
  * entry point exists for callers that cannot allocate device memory, such

@@ -10,6 +10,13 @@ the library cannot be loaded, every call raises.
     Y = linear(X, packed, scales, bias)  # X: [M, K] fp16 -> Y: [M, N] fp16
 
 ``W8A16Linear`` bundles the three for a weight that is reused.
+
+With int8 activations (one scale per token) on the same packed weight:
+
+    xq, xs, sums = quantize_tokens(X)                      # X: [M, K] fp16/fp32
+    Y = linear_w8a8(xq, xs, sums, packed, scales, bias)    # -> [M, N] fp16
+    xq, xs, sums = swiglu_quantize_tokens(Y)               # gated MLP: [M, N/2]
+    Y = linear_w8a8_grouped(xq, xs, sums, offsets, packed, scales)   # experts
 """
 from __future__ import annotations
 
@@ -19,7 +26,8 @@ import threading
 
 __all__ = [
     "W8Error", "load_library", "library_path", "quantize", "quantize_batched", "quantize_asym", "quantize_clip", "quantize_outliers", "prepack", "unpack",
-    "prepacked_bytes", "workspace_bytes", "linear", "linear_asym", "linear_outliers", "linear_decode_static", "W8A16Linear", "device_status",
+    "prepacked_bytes", "workspace_bytes", "linear", "linear_asym", "linear_outliers", "linear_decode_static", "W8A16Linear",
+    "quantize_tokens", "swiglu_quantize_tokens", "linear_w8a8", "linear_w8a8_grouped", "W8A8Linear", "device_status",
     "test_bounded_wait", "STATUS",
 ]
 
@@ -80,6 +88,12 @@ def load_library():
         lib.w8a16_workspace_bytes.restype = sz
         lib.w8a16_linear.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
         lib.w8a16_linear_decode_static.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp]
+        lib.w8_quantize_per_token.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp]
+        lib.w8_swiglu_quantize_per_token.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp, vp]
+        lib.w8a8_workspace_bytes.argtypes = [i64, i64, i64]
+        lib.w8a8_workspace_bytes.restype = sz
+        lib.w8a8_linear.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
+        lib.w8a8_linear_grouped.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
         lib.w8_error_string.argtypes = [i32]
         lib.w8_error_string.restype = ctypes.c_char_p
         lib.w8_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
@@ -87,7 +101,8 @@ def load_library():
         lib.w8_test_set_decode_helper_delay.argtypes = [ctypes.c_uint64]
         lib.w8_version.argtypes = []
         for f in ("w8_quantize_per_channel", "w8_prepack", "w8_unpack", "w8a16_linear",
-                  "w8a16_linear_decode_static",
+                  "w8a16_linear_decode_static", "w8_quantize_per_token", "w8_swiglu_quantize_per_token",
+                  "w8a8_linear", "w8a8_linear_grouped",
                   "w8_device_status", "w8_test_bounded_wait", "w8_test_set_decode_helper_delay",
                   "w8_version"):
             getattr(lib, f).restype = i32
@@ -447,6 +462,209 @@ class W8A16Linear:
 
     def __call__(self, X, out=None):
         return linear(X, self.packed, self.scales, self.bias, out=out)
+
+
+# ---------------------------------------------------------------- int8 activations
+def _need(t, name, dtype, shape, device):
+    """t is a contiguous tensor of this dtype and shape on this device."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name):
+    """Elements between the rows of a 2-D CUDA tensor with contiguous rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _pitch(K):
+    return (K + 15) // 16 * 16
+
+
+def _call(fn, what, device, *args):
+    """fn(*args, current stream of device) with that device current."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != 0:
+        raise W8Error(rc, what)
+
+
+_ws_need = {}
+
+
+def _w8a8_workspace(device, M, K, N, workspace):
+    """The scratch of a linear_w8a8 call.  Without one from the caller: the
+    stream's default buffer, or, while a graph is captured, memory of that
+    graph (two graphs replayed at once must not share it) whose counters
+    the graph itself clears."""
+    torch = _torch()
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {device}")
+        return workspace
+    need = _ws_need.get((device, N))
+    if need is None:
+        with torch.cuda.device(device):
+            need = _ws_need[(device, N)] = int(load_library().w8a8_workspace_bytes(max(M, 1), K, N))
+    if not torch.cuda.is_current_stream_capturing():
+        return _workspace(device, need)
+    sms = torch.cuda.get_device_properties(device).multi_processor_count
+    counters = max((N + 127) // 128, 2 * sms) * 4
+    workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+    workspace[need - (counters + 255) // 256 * 256:].zero_()
+    return workspace
+
+
+def _token_outputs(M, K, device, q, scales, sums):
+    torch = _torch()
+    if q is None:
+        q = torch.empty((M, _pitch(K)), dtype=torch.int8, device=device)[:, :K]
+    elif q.dtype != torch.int8 or q.shape != (M, K) or q.device != device:
+        raise ValueError(f"q must be {(M, K)} int8 on {device}")
+    ldq = _rows(q, "q") if M > 1 else _pitch(K)
+    if scales is None:
+        scales = torch.empty((M,), dtype=torch.float32, device=device)
+    else:
+        _need(scales, "scales", torch.float32, (M,), device)
+    if sums is None:
+        sums = torch.empty((M,), dtype=torch.int32, device=device)
+    else:
+        _need(sums, "sums", torch.int32, (M,), device)
+    return q, ldq, scales, sums
+
+
+def quantize_tokens(X, q=None, scales=None, sums=None):
+    """Per-token symmetric int8 quantization of X [M, K] fp16 or fp32.
+
+    Rows of X may be strided (columns contiguous).  Returns (q int8 [M, K],
+    scales fp32 [M], sums int32 [M], the sum of each row's codes).  The rows
+    of q start on 16-byte boundaries: for K % 16 != 0 it is a view of a wider
+    buffer.
+    """
+    torch = _torch()
+    lib = load_library()
+    ldx = _rows(X, "X")
+    if X.dtype == torch.float16:
+        dt = W8_F16
+    elif X.dtype == torch.float32:
+        dt = W8_F32
+    else:
+        raise ValueError("X must be float32 or float16")
+    M, K = X.shape
+    dev = X.device
+    q, ldq, scales, sums = _token_outputs(M, K, dev, q, scales, sums)
+    _call(lib.w8_quantize_per_token, "w8_quantize_per_token", dev, X.data_ptr(), dt, ldx, M, K, q.data_ptr(), ldq,
+          scales.data_ptr(), sums.data_ptr())
+    return q, scales, sums
+
+
+def swiglu_quantize_tokens(H, q=None, scales=None, sums=None):
+    """Per-token int8 quantization of silu(gate) * up for H [M, 2K] fp16, the
+    gate in the first K columns.  Returns what quantize_tokens returns, for
+    K columns."""
+    torch = _torch()
+    lib = load_library()
+    ldh = _rows(H, "H")
+    if H.dtype != torch.float16 or H.shape[1] % 2 != 0:
+        raise ValueError("H must be [M, 2K] float16")
+    M, K = H.shape[0], H.shape[1] // 2
+    dev = H.device
+    q, ldq, scales, sums = _token_outputs(M, K, dev, q, scales, sums)
+    _call(lib.w8_swiglu_quantize_per_token, "w8_swiglu_quantize_per_token", dev, H.data_ptr(), ldh, M, K, q.data_ptr(),
+          ldq, scales.data_ptr(), sums.data_ptr())
+    return q, scales, sums
+
+
+def _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, lead):
+    """Checks of both W8A8 linears; lead: () or (groups,), the leading
+    dimension of the weight's tensors."""
+    torch = _torch()
+    ldq = _rows(q, "q")
+    if q.dtype != torch.int8:
+        raise ValueError("q must be [M, K] int8")
+    M, K = q.shape
+    dev = q.device
+    if M <= 1:
+        ldq = _pitch(K)
+    N = scales.shape[-1]
+    _need(x_scales, "x_scales", torch.float32, (M,), dev)
+    _need(x_sums, "x_sums", torch.int32, (M,), dev)
+    _need(scales, "scales", torch.float16, lead + (N,), dev)
+    _need(packed, "packed", torch.uint8, lead + ((N + 127) // 128 * ((K + 63) // 64) * 8192,), dev)
+    if bias is not None:
+        _need(bias, "bias", torch.float16, lead + (N,), dev)
+    if zeros is not None:
+        _need(zeros, "zeros", torch.int8, lead + (N,), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float16, device=dev)
+    else:
+        _need(out, "out", torch.float16, (M, N), dev)
+    return ldq, M, K, N, out
+
+
+def linear_w8a8(q, x_scales, x_sums, packed, scales, bias=None, zeros=None, out=None, workspace=None):
+    """Y [M, N] fp16 = x_scales scales (q . (w - zeros)) (+ bias) for the
+    output of quantize_tokens (or of swiglu_quantize_tokens) and a packed
+    weight; zeros for codes from quantize_asym."""
+    lib = load_library()
+    ldq, M, K, N, out = _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, ())
+    dev = q.device
+    ws = _w8a8_workspace(dev, M, K, N, workspace)
+    _call(lib.w8a8_linear, "w8a8_linear", dev, q.data_ptr(), ldq, x_scales.data_ptr(), x_sums.data_ptr(),
+          packed.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+          None if bias is None else bias.data_ptr(), out.data_ptr(), M, K, N, ws.data_ptr(), ws.numel() * ws.element_size())
+    return out
+
+
+def linear_w8a8_grouped(q, x_scales, x_sums, offsets, packed, scales, bias=None, zeros=None, out=None,
+                        workspace=None):
+    """linear_w8a8 with one weight per group of rows: rows [offsets[e],
+    offsets[e + 1]) of q times weight e.  offsets: int32 [E + 1] on the device
+    (never read by the host); packed: uint8 [E, prepacked_bytes(K, N)];
+    scales, bias, zeros: [E, N].  Rows of ``out`` outside [offsets[0],
+    offsets[E]) are left as they were (uninitialised without ``out``)."""
+    torch = _torch()
+    lib = load_library()
+    if scales.dim() != 2:
+        raise ValueError("scales must be [E, N] float16")
+    E = scales.shape[0]
+    ldq, M, K, N, out = _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, (E,))
+    dev = q.device
+    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
+    ws = _w8a8_workspace(dev, M, K, N, workspace)
+    _call(lib.w8a8_linear_grouped, "w8a8_linear_grouped", dev, q.data_ptr(), ldq, x_scales.data_ptr(),
+          x_sums.data_ptr(), offsets.data_ptr(), E, packed.data_ptr(), scales.data_ptr(),
+          None if zeros is None else zeros.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(),
+          M, K, N, ws.data_ptr(), ws.numel() * ws.element_size())
+    return out
+
+
+class W8A8Linear:
+    """A linear layer whose weight W [K, N] is stored as int8 + fp16 scales
+    and whose activations are quantized per token on every call."""
+
+    def __init__(self, W, bias=None):
+        q, self.scales = quantize(W)
+        self.K, self.N = W.shape
+        self.packed = prepack(q)
+        self.bias = bias
+
+    def __call__(self, X, out=None):
+        q, x_scales, x_sums = quantize_tokens(X)
+        return linear_w8a8(q, x_scales, x_sums, self.packed, self.scales, self.bias, out=out)
 
 
 def device_status(device=None) -> int:

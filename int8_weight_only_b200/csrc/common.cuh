@@ -54,6 +54,11 @@ enum WaitSite : unsigned {
     SITE_CLIP_EMPTY = 0x50,
     SITE_CLIP_LOAD = 0x51,
     SITE_CLIP_DRAIN = 0x52,
+    SITE_I8_EMPTY = 0x60,
+    SITE_I8_FULL = 0x61,
+    SITE_I8_DEMPTY = 0x62,
+    SITE_I8_DFULL = 0x63,
+    SITE_I8_DRAIN = 0x64,
     SITE_SELFTEST = 0xEE,
 };
 
@@ -606,6 +611,53 @@ __device__ __forceinline__ uint64_t smem_desc_kmajor_sw128(uint32_t smem_addr) {
     d |= (uint64_t)1u << 46;
     d |= (uint64_t)2u << 61;
     return d;
+}
+
+// The same for a tile with 64-byte swizzle (the packed weight tile: rows of
+// 64 bytes, 16-byte chunk c of row r at slot c XOR ((r >> 1) & 3)): 8-row
+// groups 512 bytes apart, layout type 4.
+__device__ __forceinline__ uint64_t smem_desc_kmajor_sw64(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1u << 16;
+    d |= (uint64_t)(512u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)4u << 61;
+    return d;
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc], kind::i8 (8-bit integers, 32-bit
+// integer accumulator), K = 32.
+__device__ __forceinline__ void tc_mma_ss_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor for kind::i8: A unsigned 8-bit (a_format, bits 7-9,
+// 0), B signed 8-bit (b_format, bits 10-12, 1), 32-bit integer accumulator
+// (c_format, bits 4-5, 2) without saturation (bit 3), both operands K-major,
+// shape M x N.
+__host__ __device__ constexpr uint32_t idesc_u8_s8_s32(uint32_t m, uint32_t n) {
+    return (2u << 4) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// Load 16 columns of this warp's 32 lanes and wait for them, in one asm
+// statement (see tmem_load_32).
+__device__ __forceinline__ void tmem_load_16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
 }
 
 // Instruction descriptor for kind::f16: fp16 A and B, fp32 accumulator,

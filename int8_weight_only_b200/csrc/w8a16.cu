@@ -42,6 +42,9 @@ struct DeviceInfo {
     std::map<std::pair<const void *, int>, int> dclusters;
 };
 
+// Kernel attributes of the int8-activation operators (w8a8_api.cuh).
+cudaError_t w8a8_attributes();
+
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
 
@@ -103,6 +106,7 @@ int device_info(DeviceInfo **out) {
             smem((const void *)clip::percentile_quantize_kernel<__half, false>, clip::kSmemBytes);
             smem((const void *)clip::percentile_quantize_kernel<float, true>, clip::kSmemBytes);
             smem((const void *)clip::percentile_quantize_kernel<__half, true>, clip::kSmemBytes);
+            if (e == cudaSuccess) e = w8a8_attributes();
             if (e != cudaSuccess) return cuda_fail();
         }
         d.ready = true;
@@ -941,6 +945,9 @@ int w8_device_status(void *stream, uint32_t *out) {
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- int8 activations
+#include "w8a8_api.cuh"
 
 // ---------------------------------------------------------------- allocation-free decode
 // w8a16_linear_decode_static: the decode kernel with its split-K scratch in

@@ -1,0 +1,368 @@
+// W8A8 linear: Y[m,n] = s_m s_n sum_k x[m,k] (w[k,n] - z_n) + bias_n with int8
+// activations x (scale s_m per token) and int8 weights w (scale s_n and zero
+// point z_n per channel), one weight or one per group of tokens (experts).
+//
+// The packed weight tile holds the bytes u = w + 128 of 128 channels x 64
+// features as rows of 64 bytes in the 64-byte-swizzle order, so a tile copied
+// to shared memory is an operand of the 8-bit integer tensor-core product as
+// it stands: A (unsigned, the 128 channels), B (signed, the tokens), exact
+// sums in 32-bit integers in tensor memory.  No weight is ever converted:
+//   sum_k x (w - z) = sum_k x u - (128 + z) sum_k x
+// and sum_k x, one integer per token, comes with the activations.
+//
+// Work: the 8 KB weight tiles of all output tiles (128 channels x TN tokens),
+// numbered output tile by output tile, are split evenly over the thread
+// blocks, so a block's share is a run of consecutive tiles and at most its
+// first and last output tile are shared with other blocks.  Shared output
+// tiles meet in the workspace: each block stores its 32-bit integer part, the
+// last to arrive adds the parts.  Integer sums: the order changes nothing.
+//
+// Roles: warp 0 producer (weight tiles by one bulk copy, tokens by TMA),
+// warp 1 issues the products, warp 2 owns the tensor memory, warps 4-7 scale
+// and store.
+#pragma once
+
+#include <type_traits>
+
+#include "common.cuh"
+
+namespace w8 {
+namespace w8a8 {
+
+constexpr int kBN = 128;                 // channels of an output tile
+constexpr int kTile = 8192;              // packed weight tile, 128 x 64
+constexpr int kStep = 4;                 // weight tiles per stage (256 features)
+constexpr int kWBytes = kStep * kTile;
+constexpr int kThreads = 256;
+constexpr int kEpiWarps = 4;
+constexpr int kMaxGroups = 1024;
+
+template <int TN>
+struct Cfg {
+    static constexpr int kXBox = TN * 128;                   // TN tokens x 128 features
+    static constexpr int kXBytes = (kStep / 2) * kXBox;
+    static constexpr int kStageBytes = kWBytes + kXBytes;
+    static constexpr int kStages = TN <= 16 ? 6 : TN <= 32 ? 5 : TN <= 64 ? 4 : TN <= 128 ? 3 : 2;
+    static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+    static constexpr uint32_t kTmemCols = 2 * TN < 32 ? 32 : 2 * TN;
+    static_assert(kXBox % 1024 == 0, "swizzle alignment");
+    static_assert(kSmemBytes <= 217 * 1024, "shared memory budget");
+};
+
+struct Params {
+    const uint8_t *packed;     // [groups] packed weights
+    const uint16_t *scales;    // [groups][N]
+    const int8_t *zeros;       // [groups][N] or null
+    const uint16_t *bias;      // [groups][N] or null
+    const float *x_scales;     // [rows]
+    const int32_t *x_sums;     // [rows]
+    const int32_t *offsets;    // [groups + 1] first rows of the groups, or null: one group of all rows
+    uint16_t *Y;               // [rows][N]
+    int32_t *partials;         // [blocks][2 slots][TN][128]
+    int *counters;             // [blocks], zero between calls
+    int64_t rows;
+    int64_t N;
+    int groups;
+    int NB;                    // ceil(N / 128)
+    int KB;                    // ceil(K / 64)
+};
+
+// The groups' rows and token tiles, in shared memory.
+struct Groups {
+    int first[kMaxGroups + 1];    // first row, within [0, rows]
+    int tiles[kMaxGroups + 1];    // token tiles of all groups before
+};
+struct OneGroup {};
+
+// A run of weight tiles of one output tile.
+struct Seg {
+    int group, nb, tt;
+    int kb0, kb1;
+    int64_t unit;      // the output tile's number
+};
+
+template <int TN, bool kGrouped>
+struct Sched {
+    const Groups *g;
+    int NB, KB;
+    int tt_all;             // token tiles when there is one group
+    int64_t it, end, unit;
+    int kb, group;
+    __device__ Sched(const Params &p, const Groups *groups, int64_t items, int64_t G) : g(groups), NB(p.NB), KB(p.KB) {
+        const int64_t c = min64(blockIdx.x, G);   // blocks past G: an empty run
+        tt_all = kGrouped ? 0 : (int)((p.rows + TN - 1) / TN);
+        it = c * items / G;
+        end = c < G ? (c + 1) * items / G : it;
+        unit = it / KB;
+        kb = (int)(it - unit * KB);
+        group = 0;
+    }
+    __device__ bool next(Seg &s) {
+        if (it >= end) return false;
+        int64_t local = unit;
+        int tt_n = tt_all;
+        if constexpr (kGrouped) {
+            while (unit >= (int64_t)NB * g->tiles[group + 1]) ++group;
+            local -= (int64_t)NB * g->tiles[group];
+            tt_n = g->tiles[group + 1] - g->tiles[group];
+        }
+        s.group = group;
+        s.nb = (int)(local / tt_n);
+        s.tt = (int)(local - (int64_t)s.nb * tt_n);
+        s.unit = unit;
+        s.kb0 = kb;
+        s.kb1 = (int)min64(KB, kb + (end - it));
+        it += s.kb1 - s.kb0;
+        kb = 0;
+        ++unit;
+        return true;
+    }
+};
+
+template <int TN, bool kGrouped>
+__global__ void __launch_bounds__(kThreads, 1)
+w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ Params p) {
+    using C = Cfg<TN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ uint64_t full[C::kStages], empty[C::kStages];
+    __shared__ uint64_t d_full[2], d_empty[2], drain;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int last_sh;
+    using GroupsSh = typename std::conditional<kGrouped, Groups, OneGroup>::type;
+    __shared__ GroupsSh groups_sh;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&d_full[i], 1);
+            mbar_init(&d_empty[i], kEpiWarps);
+        }
+        mbar_init(&drain, 1);
+        fence_barrier_init();
+        prefetch_tensormap(&tmap_x);
+    }
+    if (warp == 2) {
+        tmem_alloc(&tmem_base_sh, C::kTmemCols);
+        tmem_relinquish();
+    }
+    pdl_launch_dependents();
+    const Groups *groups = nullptr;
+    int64_t items;
+    if constexpr (kGrouped) {
+        // first rows clamped to [0, rows], so no offset can lead out of bounds
+        pdl_wait();
+        groups = reinterpret_cast<const Groups *>(&groups_sh);
+        for (int e = threadIdx.x; e <= p.groups; e += kThreads)
+            groups_sh.first[e] = (int)max64(0, min64(p.rows, p.offsets[e]));
+        __syncthreads();
+        if (warp == 0) {
+            int before = 0;
+            if (lane == 0) groups_sh.tiles[0] = 0;
+            for (int e0 = 0; e0 < p.groups; e0 += 32) {
+                const int e = e0 + lane;
+                int n = 0;
+                if (e < p.groups) n = (max(0, groups_sh.first[e + 1] - groups_sh.first[e]) + TN - 1) / TN;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, n, d);
+                    if (lane >= d) n += o;
+                }
+                if (e < p.groups) groups_sh.tiles[e + 1] = before + n;
+                before += __shfl_sync(0xffffffffu, n, 31);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+    if constexpr (kGrouped) {
+        items = (int64_t)groups->tiles[p.groups] * p.NB * p.KB;
+    } else {
+        items = (p.rows + TN - 1) / TN * p.NB * p.KB;
+    }
+    // blocks with work: every one of them has at least one weight tile
+    const int64_t G = max64(1, min64(gridDim.x, items));
+    // rows of a segment's token tile: the first, and how many of the group's
+    auto rows_of = [&](const Seg &s, int64_t &row0) -> int {
+        int64_t first = 0, end = p.rows;
+        if constexpr (kGrouped) {
+            first = groups->first[s.group];
+            end = groups->first[s.group + 1];
+        }
+        row0 = first + (int64_t)s.tt * TN;
+        return (int)min64(TN, end - row0);
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------- producer
+        if (lane == 0) {
+            pdl_wait();
+            int st = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            Sched<TN, kGrouped> sched(p, groups, items, G);
+            Seg sg;
+            while (ok && sched.next(sg)) {
+                int64_t row0;
+                rows_of(sg, row0);
+                const uint8_t *w = p.packed + ((int64_t)sg.group * p.NB + sg.nb) * p.KB * kTile;
+                for (int kb = sg.kb0; kb < sg.kb1; kb += kStep) {
+                    const int cnt = min(kStep, sg.kb1 - kb), boxes = (cnt + 1) >> 1;
+                    if (!mbar_wait(&empty[st], ph ^ 1u, SITE_I8_EMPTY)) { ok = false; break; }
+                    uint8_t *ws = ring + st * C::kStageBytes, *xs = ws + kWBytes;
+                    mbar_arrive_expect_tx(&full[st], cnt * kTile + boxes * C::kXBox);
+                    bulk_g2s(ws, w + (int64_t)kb * kTile, cnt * kTile, &full[st]);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(xs + b * C::kXBox, &tmap_x, (kb + 2 * b) * 64, (int)row0, &full[st]);
+                    ++issued;
+                    if (++st == C::kStages) { st = 0; ph ^= 1u; }
+                }
+            }
+            // every copy has landed before the block can leave
+            for (int i = 0; i < C::kStages && i < issued; ++i) {
+                if (--st < 0) { st = C::kStages - 1; ph ^= 1u; }
+                mbar_wait(&full[st], ph, SITE_I8_DRAIN, 10000000ull);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------- products
+        if (lane == 0) {
+            int st = 0, d = 0;
+            uint32_t ph = 0, dph = 0;
+            bool ok = true;
+            Sched<TN, kGrouped> sched(p, groups, items, G);
+            Seg sg;
+            while (ok && sched.next(sg)) {
+                int64_t row0;
+                const int n = (rows_of(sg, row0) + 15) & ~15;
+                const uint32_t idesc = idesc_u8_s8_s32(kBN, n);
+                if (!mbar_wait(&d_empty[d], dph ^ 1u, SITE_I8_DEMPTY)) { ok = false; break; }
+                tc_fence_after();
+                for (int kb = sg.kb0; kb < sg.kb1; kb += kStep) {
+                    const int cnt = min(kStep, sg.kb1 - kb);
+                    if (!mbar_wait(&full[st], ph, SITE_I8_FULL)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t wa = smem_u32(ring + st * C::kStageBytes), xa = wa + kWBytes;
+                    for (int t = 0; t < cnt; ++t) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            tc_mma_ss_i8(tmem + d * TN, smem_desc_kmajor_sw64(wa + t * kTile + 32 * j),
+                                         smem_desc_kmajor_sw128(xa + (t >> 1) * C::kXBox + (t & 1) * 64 + 32 * j), idesc,
+                                         ((kb - sg.kb0) | t | j) != 0);
+                    }
+                    tc_commit(&empty[st]);
+                    if (++st == C::kStages) { st = 0; ph ^= 1u; }
+                }
+                if (!ok) break;
+                tc_commit(&d_full[d]);
+                if (++d == 2) { d = 0; dph ^= 1u; }
+            }
+            // every product is complete before the tensor memory is freed
+            tc_commit(&drain);
+            mbar_wait(&drain, 0, SITE_I8_DRAIN);
+        }
+    } else if (warp >= 4) {
+        // ---------------------------------------------------- scale and store
+        pdl_wait();
+        const int q4 = warp & 3;
+        const int r = 32 * q4 + lane;
+        int d = 0;
+        uint32_t dph = 0;
+        Sched<TN, kGrouped> sched(p, groups, items, G);
+        Seg sg;
+        while (sched.next(sg)) {
+            int64_t row0;
+            const int nr = rows_of(sg, row0);
+            const int64_t n = (int64_t)sg.nb * kBN + r;
+            const bool n_ok = n < p.N;
+            const int64_t ch = (int64_t)sg.group * p.N + n;
+            const float sc = n_ok ? __half2float(__ushort_as_half(p.scales[ch])) : 0.0f;
+            const float bi = (n_ok && p.bias) ? __half2float(__ushort_as_half(p.bias[ch])) : 0.0f;
+            const int off = 128 + ((n_ok && p.zeros) ? (int)p.zeros[ch] : 0);
+            // scale 16 tokens' sums and store them
+            auto store16 = [&](const uint32_t (&v)[16], int c0) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (c0 + i < nr) {
+                        const int64_t m = row0 + c0 + i;
+                        const int acc = (int)v[i] - off * p.x_sums[m];
+                        const float y = fmaf(__fmul_rn((float)acc, p.x_scales[m]), sc, bi);
+                        if (n_ok) p.Y[m * p.N + n] = __half_as_ushort(__float2half_rn(y));
+                    }
+                }
+            };
+            // all four warps give up together: they meet at barriers below
+            if (!named_bar_all(1, 32 * kEpiWarps, mbar_wait(&d_full[d], dph, SITE_I8_DFULL))) break;
+            tc_fence_after();
+            const uint32_t src = tmem + ((uint32_t)(32 * q4) << 16) + d * TN;
+            const bool whole = sg.kb0 == 0 && sg.kb1 == p.KB;
+            int32_t *mine = nullptr;
+            if (!whole) {
+                const int64_t begin = (int64_t)blockIdx.x * items / G;
+                mine = p.partials + ((int64_t)blockIdx.x * 2 + (begin / p.KB == sg.unit ? 0 : 1)) * (TN * kBN) + r;
+            }
+            for (int c0 = 0; c0 < nr; c0 += 16) {
+                uint32_t v[16];
+                tmem_load_16(src + c0, v);
+                if (whole) {
+                    store16(v, c0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) __stcg(mine + (c0 + i) * kBN, (int32_t)v[i]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&d_empty[d]);
+            if (++d == 2) { d = 0; dph ^= 1u; }
+            if (!whole) {
+                // blocks that share this output tile: the owners of its first
+                // to last weight tile; the first one's counter is the tile's
+                const int64_t it0 = sg.unit * p.KB;
+                const int64_t j0 = ((it0 + 1) * G - 1) / items, j1 = ((it0 + p.KB) * G - 1) / items;
+                named_bar_sync(1, 32 * kEpiWarps);   // the part is written
+                if (threadIdx.x == 128) {
+                    const int have = atomic_add_acq_rel_gpu(p.counters + j0, 1) + 1;
+                    const int last = have == (int)(j1 - j0) + 1;
+                    if (last) p.counters[j0] = 0;
+                    last_sh = last;
+                }
+                named_bar_sync(1, 32 * kEpiWarps);
+                if (last_sh) {
+                    for (int c0 = 0; c0 < nr; c0 += 16) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = 0;
+                        for (int64_t j = j0; j <= j1; ++j) {
+                            const int64_t begin = j * items / G;
+                            const int32_t *part =
+                                p.partials + (j * 2 + (begin / p.KB == sg.unit ? 0 : 1)) * (TN * kBN) + r;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] += (uint32_t)__ldcg(part + (c0 + i) * kBN);
+                        }
+                        store16(v, c0);
+                    }
+                }
+                named_bar_sync(1, 32 * kEpiWarps);   // last_sh is read by all
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+}  // namespace w8a8
+}  // namespace w8

@@ -1,0 +1,212 @@
+// Entry points of the int8-activation operators (per-token quantization, the
+// W8A8 linear and its grouped form).  Included by w8a16.cu after its helpers
+// (device_info, tensor maps, alignment and overlap checks).
+#pragma once
+
+#include "tokens.cuh"
+#include "w8a8.cuh"
+
+namespace {
+
+// Sums of 128 x 255 x K must stay below 2^31.
+constexpr int64_t kMaxSumK = 65536;
+// Rows of a grouped call: the token tiles of 1024 groups stay below 2^31
+// whatever the offsets on the device are.
+constexpr int64_t kMaxGroupedRows = 1 << 24;
+
+// Bytes from the first to past the last element of `rows` rows of `width`
+// elements, `pitch` elements apart.
+inline size_t span(int64_t rows, int64_t pitch, int64_t width, size_t elem) {
+    return rows < 1 ? 0 : ((size_t)(rows - 1) * (size_t)pitch + (size_t)width) * elem;
+}
+
+// ---------------------------------------------------------------- per-token quantization
+template <int kSrc, int TPR, int V>
+int launch_tokens_as(const tokens::Params &p, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(TPR == 32 ? cdiv(p.M, 8) : p.M), 1, 1);
+    cfg.blockDim = dim3(tokens::kBlock<TPR>, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, tokens::quantize_tokens_kernel<kSrc, TPR, V>, p) != cudaSuccess) return cuda_fail();
+    return launch_status();
+}
+
+template <int kSrc>
+int launch_tokens(const tokens::Params &p, cudaStream_t st) {
+    if (p.K <= 512) return launch_tokens_as<kSrc, 32, 2>(p, st);
+    if (p.K <= 4096) return launch_tokens_as<kSrc, 256, 2>(p, st);
+    if (p.K <= 16384) return launch_tokens_as<kSrc, 512, 4>(p, st);
+    return launch_tokens_as<kSrc, 512, 0>(p, st);
+}
+
+// x_cols: elements of a row that are read (K, or 2K for the SwiGLU).
+int tokens_common(const void *X, int dtype, bool swiglu, int64_t ldx, int64_t M, int64_t K, int8_t *q, int64_t ldq,
+                  float *scales, int32_t *sums, void *stream) {
+    if (dtype != W8_F32 && dtype != W8_F16) return W8_ERR_DTYPE;
+    const int64_t cols = swiglu ? 2 * K : K;
+    if (M < 0 || K < 1 || K % 8 != 0 || M > (int64_t)INT32_MAX || K > (int64_t)INT32_MAX / 2 || ldx < cols || ldq < K ||
+        ldq % 16 != 0 || ldx > (1LL << 40) || ldq > (1LL << 40))
+        return W8_ERR_SHAPE;
+    if (M == 0) return W8_OK;
+    if (!X || !q || !scales || !sums) return W8_ERR_NULL;
+    const size_t elem = dtype == W8_F32 ? 4 : 2;
+    if (!aligned16(X) || !aligned16(q) || !aligned16(scales) || !aligned16(sums) || (M > 1 && ldx * elem % 16 != 0))
+        return W8_ERR_ALIGN;
+    const size_t xb = span(M, ldx, cols, elem), qb = span(M, ldq, K, 1), sb = (size_t)M * 4;
+    if (overlap(X, xb, q, qb) || overlap(X, xb, scales, sb) || overlap(X, xb, sums, sb) || overlap(q, qb, scales, sb) ||
+        overlap(q, qb, sums, sb) || overlap(scales, sb, sums, sb))
+        return W8_ERR_ALIAS;
+    DeviceInfo *d = nullptr;
+    const int rc = device_info(&d);
+    if (rc != W8_OK) return rc;
+    const tokens::Params p = {X, ldx, M, K, q, ldq, scales, sums};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (swiglu) return launch_tokens<tokens::kSwiglu>(p, st);
+    return dtype == W8_F32 ? launch_tokens<tokens::kF32>(p, st) : launch_tokens<tokens::kF16>(p, st);
+}
+
+// ---------------------------------------------------------------- W8A8 linear
+template <int TN, bool kGrouped>
+int launch_w8a8_as(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
+    CUtensorMap map;
+    auto fn = encode_fn();
+    if (!fn) return W8_ERR_CUDA;
+    // codes [rows, K], box 128 features x TN rows, 128-byte swizzle; features
+    // past K and rows past the last read as zero
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)p.rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ldq};
+    cuuint32_t box[2] = {128, (cuuint32_t)TN};
+    cuuint32_t estr[2] = {1, 1};
+    if (fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(q), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return W8_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    // one block per multiprocessor, as far as the workspace has room for
+    // the two shared output tiles of each
+    const int64_t slots = (int64_t)(partial_area_bytes(d->sms) / (2 * (size_t)TN * w8a8::kBN * sizeof(int32_t)));
+    cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(d->sms, slots)), 1, 1);
+    cfg.blockDim = dim3(w8a8::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = w8a8::Cfg<TN>::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, w8a8::w8a8_kernel<TN, kGrouped>, map, p) != cudaSuccess) return cuda_fail();
+    return launch_status();
+}
+
+template <bool kGrouped>
+int launch_w8a8(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, int64_t tokens,
+                cudaStream_t st) {
+    if (tokens <= 16) return launch_w8a8_as<16, kGrouped>(d, q, ldq, K, p, st);
+    if (tokens <= 32) return launch_w8a8_as<32, kGrouped>(d, q, ldq, K, p, st);
+    if (tokens <= 64) return launch_w8a8_as<64, kGrouped>(d, q, ldq, K, p, st);
+    if (tokens <= 128) return launch_w8a8_as<128, kGrouped>(d, q, ldq, K, p, st);
+    return launch_w8a8_as<256, kGrouped>(d, q, ldq, K, p, st);
+}
+
+cudaError_t w8a8_attributes() {
+    cudaError_t e = cudaSuccess;
+#define W8_I8_SMEM(TN)                                                                                        \
+    for (const void *f : {(const void *)w8a8::w8a8_kernel<TN, false>, (const void *)w8a8::w8a8_kernel<TN, true>}) \
+        if (e == cudaSuccess)                                                                                 \
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, w8a8::Cfg<TN>::kSmemBytes);
+    W8_I8_SMEM(16)
+    W8_I8_SMEM(32)
+    W8_I8_SMEM(64)
+    W8_I8_SMEM(128)
+    W8_I8_SMEM(256)
+#undef W8_I8_SMEM
+    return e;
+}
+
+// The linear of one weight (offsets == nullptr, groups == 1) or of one weight
+// per group.
+int w8a8_common(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums, const int32_t *offsets,
+                bool grouped, int64_t groups, const uint8_t *packed, const uint16_t *scales, const int8_t *zeros,
+                const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K, int64_t N, void *workspace,
+                size_t workspace_bytes, void *stream) {
+    if (M < 0 || K < 1 || N < 1 || K % 8 != 0 || N % 8 != 0 || K > kMaxSumK || M > (int64_t)INT32_MAX - 512 ||
+        N > (1LL << 30) || ldq < K || ldq % 16 != 0 || ldq >= (1LL << 40))
+        return W8_ERR_SHAPE;
+    if (grouped && (groups < 1 || groups > w8a8::kMaxGroups || M > kMaxGroupedRows)) return W8_ERR_SHAPE;
+    if (!packed || !scales || (grouped && !offsets)) return W8_ERR_NULL;
+    if (M == 0) return W8_OK;   // no rows: nothing to read or write
+    if (!q || !x_scales || !x_sums || !Y) return W8_ERR_NULL;
+    if (!aligned16(q) || !aligned16(x_scales) || !aligned16(x_sums) || !aligned16(packed) || !aligned16(scales) ||
+        !aligned16(Y) || (bias && !aligned16(bias)) || (zeros && !aligned16(zeros)) || (offsets && !aligned16(offsets)) ||
+        (workspace && !aligned16(workspace)))
+        return W8_ERR_ALIGN;
+    const size_t yb = (size_t)M * N * 2, qb = span(M, ldq, K, 1), wb = (size_t)groups * w8_prepacked_bytes(K, N),
+                 sb = (size_t)groups * N * 2;
+    if (overlap(Y, yb, q, qb) || overlap(Y, yb, x_scales, (size_t)M * 4) || overlap(Y, yb, x_sums, (size_t)M * 4) ||
+        overlap(Y, yb, packed, wb) || overlap(Y, yb, scales, sb) || (bias && overlap(Y, yb, bias, sb)) ||
+        (zeros && overlap(Y, yb, zeros, sb / 2)) || (grouped && overlap(Y, yb, offsets, (size_t)(groups + 1) * 4)))
+        return W8_ERR_ALIAS;
+    DeviceInfo *d = nullptr;
+    int rc = device_info(&d);
+    if (rc != W8_OK) return rc;
+    const size_t need = workspace_total(d->sms, N);
+    if (!workspace || workspace_bytes < need) return W8_ERR_WORKSPACE;
+    if (overlap(workspace, need, Y, yb) || overlap(workspace, need, q, qb)) return W8_ERR_ALIAS;
+    w8a8::Params p = {};
+    p.packed = packed;
+    p.scales = scales;
+    p.zeros = zeros;
+    p.bias = bias;
+    p.x_scales = x_scales;
+    p.x_sums = x_sums;
+    p.offsets = offsets;
+    p.Y = Y;
+    p.partials = static_cast<int32_t *>(workspace);
+    p.counters = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + partial_area_bytes(d->sms));
+    p.rows = M;
+    p.N = N;
+    p.groups = (int)groups;
+    p.NB = (int)cdiv(N, 128);
+    p.KB = (int)cdiv(K, 64);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (grouped) return launch_w8a8<true>(d, q, ldq, K, p, cdiv(M, groups), st);
+    return launch_w8a8<false>(d, q, ldq, K, p, M, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int w8_quantize_per_token(const void *X, int x_dtype, int64_t ldx, int64_t M, int64_t K, int8_t *q, int64_t ldq,
+                          float *scales, int32_t *sums, void *stream) {
+    return tokens_common(X, x_dtype, false, ldx, M, K, q, ldq, scales, sums, stream);
+}
+
+int w8_swiglu_quantize_per_token(const uint16_t *H, int64_t ldh, int64_t M, int64_t K, int8_t *q, int64_t ldq,
+                                 float *scales, int32_t *sums, void *stream) {
+    return tokens_common(H, W8_F16, true, ldh, M, K, q, ldq, scales, sums, stream);
+}
+
+size_t w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N) { return w8a16_workspace_bytes(M, K, N); }
+
+int w8a8_linear(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums, const uint8_t *packed,
+                const uint16_t *scales, const int8_t *zeros, const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K,
+                int64_t N, void *workspace, size_t workspace_bytes, void *stream) {
+    return w8a8_common(q, ldq, x_scales, x_sums, nullptr, false, 1, packed, scales, zeros, bias, Y, M, K, N, workspace,
+                       workspace_bytes, stream);
+}
+
+int w8a8_linear_grouped(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums,
+                        const int32_t *offsets, int64_t groups, const uint8_t *packed, const uint16_t *scales,
+                        const int8_t *zeros, const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K, int64_t N,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+    return w8a8_common(q, ldq, x_scales, x_sums, offsets, true, groups, packed, scales, zeros, bias, Y, M, K, N,
+                       workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
