@@ -441,6 +441,17 @@ __device__ __forceinline__ void tc_mma_ts_f16_pair(uint32_t d_tmem, uint32_t a_t
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The same for 8-bit integers, both operands in shared memory: kind::i8,
+// unsigned A, signed B, 32-bit integer accumulator, K = 32.
+__device__ __forceinline__ void tc_mma_ss_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                  uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // Arrive once on the mbarrier at `bar`'s offset in each CTA of `cta_mask`
 // when all prior pair MMAs of this thread have completed.
 __device__ __forceinline__ void tc_commit_pair_mc(uint64_t *bar, uint16_t cta_mask) {

@@ -42,7 +42,7 @@ struct Cfg {
     static constexpr int kXBox = TN * 128;                   // TN tokens x 128 features
     static constexpr int kXBytes = (kStep / 2) * kXBox;
     static constexpr int kStageBytes = kWBytes + kXBytes;
-    static constexpr int kStages = TN <= 16 ? 6 : TN <= 32 ? 5 : TN <= 64 ? 4 : TN <= 128 ? 3 : 2;
+    static constexpr int kStages = TN <= 16 ? 6 : TN <= 32 ? 5 : TN <= 64 ? 4 : 3;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
     static constexpr uint32_t kTmemCols = 2 * TN < 32 ? 32 : 2 * TN;
     static_assert(kXBox % 1024 == 0, "swizzle alignment");
@@ -73,6 +73,31 @@ struct Groups {
     int tiles[kMaxGroups + 1];    // token tiles of all groups before
 };
 struct OneGroup {};
+
+// All kThreads_ threads of the block; a block barrier has to follow.  The
+// first rows are clamped to [0, rows], so no offset can lead out of bounds.
+template <int TN, int kThreads_>
+__device__ __forceinline__ void load_groups(const Params &p, Groups &g) {
+    for (int e = threadIdx.x; e <= p.groups; e += kThreads_) g.first[e] = (int)max64(0, min64(p.rows, p.offsets[e]));
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int before = 0;
+        if (lane == 0) g.tiles[0] = 0;
+        for (int e0 = 0; e0 < p.groups; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < p.groups) n = (max(0, g.first[e + 1] - g.first[e]) + TN - 1) / TN;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, n, d);
+                if (lane >= d) n += o;
+            }
+            if (e < p.groups) g.tiles[e + 1] = before + n;
+            before += __shfl_sync(0xffffffffu, n, 31);
+        }
+    }
+}
 
 // A run of weight tiles of one output tile.
 struct Seg {
@@ -130,6 +155,8 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
     __shared__ uint64_t d_full[2], d_empty[2], drain;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int last_sh;
+    __shared__ __align__(16) int sum_sh[2][TN];       // the token tile's sums and scales
+    __shared__ __align__(16) float xs_sh[2][TN];
     using GroupsSh = typename std::conditional<kGrouped, Groups, OneGroup>::type;
     __shared__ GroupsSh groups_sh;
 
@@ -156,28 +183,9 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
     const Groups *groups = nullptr;
     int64_t items;
     if constexpr (kGrouped) {
-        // first rows clamped to [0, rows], so no offset can lead out of bounds
         pdl_wait();
+        load_groups<TN, kThreads>(p, *reinterpret_cast<Groups *>(&groups_sh));
         groups = reinterpret_cast<const Groups *>(&groups_sh);
-        for (int e = threadIdx.x; e <= p.groups; e += kThreads)
-            groups_sh.first[e] = (int)max64(0, min64(p.rows, p.offsets[e]));
-        __syncthreads();
-        if (warp == 0) {
-            int before = 0;
-            if (lane == 0) groups_sh.tiles[0] = 0;
-            for (int e0 = 0; e0 < p.groups; e0 += 32) {
-                const int e = e0 + lane;
-                int n = 0;
-                if (e < p.groups) n = (max(0, groups_sh.first[e + 1] - groups_sh.first[e]) + TN - 1) / TN;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, n, d);
-                    if (lane >= d) n += o;
-                }
-                if (e < p.groups) groups_sh.tiles[e + 1] = before + n;
-                before += __shfl_sync(0xffffffffu, n, 31);
-            }
-        }
     }
     tc_fence_before();
     __syncthreads();
@@ -287,19 +295,32 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
             const float sc = n_ok ? __half2float(__ushort_as_half(p.scales[ch])) : 0.0f;
             const float bi = (n_ok && p.bias) ? __half2float(__ushort_as_half(p.bias[ch])) : 0.0f;
             const int off = 128 + ((n_ok && p.zeros) ? (int)p.zeros[ch] : 0);
+            // the tokens' sums and scales, read while the products run; the
+            // other buffer may still be read for the tile before
+            for (int c = threadIdx.x - 128; c < TN; c += 32 * kEpiWarps) {
+                sum_sh[d][c] = c < nr ? __ldg(p.x_sums + row0 + c) : 0;
+                xs_sh[d][c] = c < nr ? __ldg(p.x_scales + row0 + c) : 0.0f;
+            }
+            uint16_t *const y0 = p.Y + row0 * p.N + n;
             // scale 16 tokens' sums and store them
             auto store16 = [&](const uint32_t (&v)[16], int c0) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (c0 + i < nr) {
-                        const int64_t m = row0 + c0 + i;
-                        const int acc = (int)v[i] - off * p.x_sums[m];
-                        const float y = fmaf(__fmul_rn((float)acc, p.x_scales[m]), sc, bi);
-                        if (n_ok) p.Y[m * p.N + n] = __half_as_ushort(__float2half_rn(y));
+                for (int i = 0; i < 16; i += 4) {
+                    const int4 sm = *reinterpret_cast<const int4 *>(&sum_sh[d][c0 + i]);
+                    const float4 xs = *reinterpret_cast<const float4 *>(&xs_sh[d][c0 + i]);
+                    const int s4[4] = {sm.x, sm.y, sm.z, sm.w};
+                    const float x4[4] = {xs.x, xs.y, xs.z, xs.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int acc = (int)v[i + j] - off * s4[j];
+                        const float y = fmaf(__fmul_rn((float)acc, x4[j]), sc, bi);
+                        if (n_ok && c0 + i + j < nr)
+                            y0[(int64_t)(c0 + i + j) * p.N] = __half_as_ushort(__float2half_rn(y));
                     }
                 }
             };
             // all four warps give up together: they meet at barriers below
+            // (this one also shows them the sums and scales)
             if (!named_bar_all(1, 32 * kEpiWarps, mbar_wait(&d_full[d], dph, SITE_I8_DFULL))) break;
             tc_fence_after();
             const uint32_t src = tmem + ((uint32_t)(32 * q4) << 16) + d * TN;
@@ -322,7 +343,6 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_empty[d]);
-            if (++d == 2) { d = 0; dph ^= 1u; }
             if (!whole) {
                 // blocks that share this output tile: the owners of its first
                 // to last weight tile; the first one's counter is the tile's
@@ -353,6 +373,7 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
                 }
                 named_bar_sync(1, 32 * kEpiWarps);   // last_sh is read by all
             }
+            if (++d == 2) { d = 0; dph ^= 1u; }
         }
     }
 

@@ -5,6 +5,7 @@
 
 #include "tokens.cuh"
 #include "w8a8.cuh"
+#include "w8a8_pair.cuh"
 
 namespace {
 
@@ -71,21 +72,26 @@ int tokens_common(const void *X, int dtype, bool swiglu, int64_t ldx, int64_t M,
 }
 
 // ---------------------------------------------------------------- W8A8 linear
+// Codes [rows, K], box 128 features x box_rows rows, 128-byte swizzle;
+// features past K and rows past the last read as zero.
+int make_map_codes(CUtensorMap *map, const int8_t *q, int64_t ldq, int64_t rows, int64_t K, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return W8_ERR_CUDA;
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ldq};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(q), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? W8_OK : W8_ERR_CUDA;
+}
+
 template <int TN, bool kGrouped>
 int launch_w8a8_as(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
     CUtensorMap map;
-    auto fn = encode_fn();
-    if (!fn) return W8_ERR_CUDA;
-    // codes [rows, K], box 128 features x TN rows, 128-byte swizzle; features
-    // past K and rows past the last read as zero
-    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)p.rows};
-    cuuint64_t strides[1] = {(cuuint64_t)ldq};
-    cuuint32_t box[2] = {128, (cuuint32_t)TN};
-    cuuint32_t estr[2] = {1, 1};
-    if (fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(q), dims, strides, box, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return W8_ERR_CUDA;
+    const int rc = make_map_codes(&map, q, ldq, p.rows, K, TN);
+    if (rc != W8_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     // one block per multiprocessor, as far as the workspace has room for
     // the two shared output tiles of each
@@ -103,14 +109,65 @@ int launch_w8a8_as(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const
     return launch_status();
 }
 
+// Many tokens: pairs of SMs (w8a8_pair.cuh).
+template <bool kGrouped>
+int launch_w8a8_pair(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
+    namespace wp = w8a8::pair;
+    CUtensorMap map_x, map_w;
+    int rc = make_map_codes(&map_x, q, ldq, p.rows, K, wp::kBT / 2);
+    if (rc != W8_OK) return rc;
+    // coordinates of rows of 128 packed bytes and tile numbers are 32-bit
+    const int64_t wrows = (int64_t)p.groups * p.NB * p.KB * (w8a8::kTile / 128);
+    const int64_t most_tiles = (cdiv(p.rows, wp::kBT) + p.groups) * cdiv(p.NB, 2);
+    if (wrows > (int64_t)INT32_MAX - 128 || most_tiles > INT32_MAX / 2) return W8_ERR_SHAPE;
+    rc = make_map_2d(&map_w, p.packed, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128, (uint64_t)wrows, 128, 128,
+                     CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (rc != W8_OK) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(wp::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = wp::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;   // the occupancy query takes the cluster shape only
+    int pairs = 0;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        int &cached = d->i8pairs[kGrouped ? 1 : 0];
+        if (cached == 0) {
+            cfg.gridDim = dim3((unsigned)d->sms, 1, 1);
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, wp::w8a8_pair_kernel<kGrouped>, &cfg) != cudaSuccess || n < 1) {
+                cudaGetLastError();
+                n = d->sms / 2;
+            }
+            cached = std::max(1, std::min(n, d->sms / 2));   // the workspace has parts for sms / 2 pairs
+        }
+        pairs = cached;
+    }
+    cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, wp::w8a8_pair_kernel<kGrouped>, map_w, map_x, p) != cudaSuccess) return cuda_fail();
+    return launch_status();
+}
+
+// More tokens (a group, on average) than this go to the pairs.
+constexpr int64_t kPairFrom = 128;
+
 template <bool kGrouped>
 int launch_w8a8(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, int64_t tokens,
                 cudaStream_t st) {
+    if (tokens > kPairFrom) return launch_w8a8_pair<kGrouped>(d, q, ldq, K, p, st);
     if (tokens <= 16) return launch_w8a8_as<16, kGrouped>(d, q, ldq, K, p, st);
     if (tokens <= 32) return launch_w8a8_as<32, kGrouped>(d, q, ldq, K, p, st);
     if (tokens <= 64) return launch_w8a8_as<64, kGrouped>(d, q, ldq, K, p, st);
-    if (tokens <= 128) return launch_w8a8_as<128, kGrouped>(d, q, ldq, K, p, st);
-    return launch_w8a8_as<256, kGrouped>(d, q, ldq, K, p, st);
+    return launch_w8a8_as<128, kGrouped>(d, q, ldq, K, p, st);
 }
 
 cudaError_t w8a8_attributes() {
@@ -123,8 +180,10 @@ cudaError_t w8a8_attributes() {
     W8_I8_SMEM(32)
     W8_I8_SMEM(64)
     W8_I8_SMEM(128)
-    W8_I8_SMEM(256)
 #undef W8_I8_SMEM
+    for (const void *f : {(const void *)w8a8::pair::w8a8_pair_kernel<false>, (const void *)w8a8::pair::w8a8_pair_kernel<true>})
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, w8a8::pair::kSmemBytes);
     return e;
 }
 
