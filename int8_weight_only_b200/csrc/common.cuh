@@ -637,6 +637,18 @@ __device__ __forceinline__ uint64_t smem_desc_kmajor_sw64(uint32_t smem_addr) {
     return d;
 }
 
+// One lane of a converged warp.  A branch on this, unlike one on the lane
+// number, keeps the operands of the instructions under it warp-uniform.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // D[tmem] (+)= A[smem desc] * B[smem desc], kind::i8 (8-bit integers, 32-bit
 // integer accumulator), K = 32.
 __device__ __forceinline__ void tc_mma_ss_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,

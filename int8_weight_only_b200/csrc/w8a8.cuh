@@ -160,7 +160,7 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
     using GroupsSh = typename std::conditional<kGrouped, Groups, OneGroup>::type;
     __shared__ GroupsSh groups_sh;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // warp-uniform
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -242,41 +242,55 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
         }
     } else if (warp == 1) {
         // ---------------------------------------------------- products
-        if (lane == 0) {
-            int st = 0, d = 0;
-            uint32_t ph = 0, dph = 0;
-            bool ok = true;
-            Sched<TN, kGrouped> sched(p, groups, items, G);
-            Seg sg;
-            while (ok && sched.next(sg)) {
-                int64_t row0;
-                const int n = (rows_of(sg, row0) + 15) & ~15;
-                const uint32_t idesc = idesc_u8_s8_s32(kBN, n);
-                if (!mbar_wait(&d_empty[d], dph ^ 1u, SITE_I8_DEMPTY)) { ok = false; break; }
+        // the whole warp walks the steps and one elected lane issues: the
+        // operands stay in uniform registers
+        int st = 0, d = 0;
+        uint32_t ph = 0, dph = 0;
+        bool ok = true;
+        const uint64_t w_desc0 = smem_desc_kmajor_sw64(smem_u32(ring));
+        const uint64_t x_desc0 = smem_desc_kmajor_sw128(smem_u32(ring) + kWBytes);
+        Sched<TN, kGrouped> sched(p, groups, items, G);
+        Seg sg;
+        while (ok && sched.next(sg)) {
+            int64_t row0;
+            const int n = (rows_of(sg, row0) + 15) & ~15;
+            const uint32_t idesc = idesc_u8_s8_s32(kBN, n);
+            const uint32_t dst = tmem + d * TN;
+            if (!warp_all(mbar_wait(&d_empty[d], dph ^ 1u, SITE_I8_DEMPTY))) { ok = false; break; }
+            tc_fence_after();
+            uint32_t acc = 0;
+            for (int kb = sg.kb0; kb < sg.kb1; kb += kStep) {
+                const int cnt = min(kStep, sg.kb1 - kb);
+                if (!warp_all(mbar_wait(&full[st], ph, SITE_I8_FULL))) { ok = false; break; }
                 tc_fence_after();
-                for (int kb = sg.kb0; kb < sg.kb1; kb += kStep) {
-                    const int cnt = min(kStep, sg.kb1 - kb);
-                    if (!mbar_wait(&full[st], ph, SITE_I8_FULL)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t wa = smem_u32(ring + st * C::kStageBytes), xa = wa + kWBytes;
-                    for (int t = 0; t < cnt; ++t) {
+                // descriptors count in units of 16 bytes; the sums stay within
+                // the address field (shared memory < 256 KB)
+                const uint64_t wd = w_desc0 + (uint32_t)st * (C::kStageBytes / 16);
+                const uint64_t xd = x_desc0 + (uint32_t)st * (C::kStageBytes / 16);
+                if (elect_one()) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            tc_mma_ss_i8(tmem + d * TN, smem_desc_kmajor_sw64(wa + t * kTile + 32 * j),
-                                         smem_desc_kmajor_sw128(xa + (t >> 1) * C::kXBox + (t & 1) * 64 + 32 * j), idesc,
-                                         ((kb - sg.kb0) | t | j) != 0);
+                    for (int t = 0; t < kStep; ++t) {
+                        if (t < cnt) {
+                            const uint64_t wt = wd + t * (kTile / 16), xt = xd + (t >> 1) * (C::kXBox / 16) + (t & 1) * 4;
+                            tc_mma_ss_i8(dst, wt, xt, idesc, t == 0 ? acc : 1);
+                            tc_mma_ss_i8(dst, wt + 2, xt + 2, idesc, 1);
+                        }
                     }
                     tc_commit(&empty[st]);
-                    if (++st == C::kStages) { st = 0; ph ^= 1u; }
                 }
-                if (!ok) break;
-                tc_commit(&d_full[d]);
-                if (++d == 2) { d = 0; dph ^= 1u; }
+                __syncwarp();
+                acc = 1;
+                if (++st == C::kStages) { st = 0; ph ^= 1u; }
             }
-            // every product is complete before the tensor memory is freed
-            tc_commit(&drain);
-            mbar_wait(&drain, 0, SITE_I8_DRAIN);
+            if (!ok) break;
+            if (elect_one()) tc_commit(&d_full[d]);
+            __syncwarp();
+            if (++d == 2) { d = 0; dph ^= 1u; }
         }
+        // every product is complete before the tensor memory is freed
+        if (elect_one()) tc_commit(&drain);
+        __syncwarp();
+        mbar_wait(&drain, 0, SITE_I8_DRAIN);
     } else if (warp >= 4) {
         // ---------------------------------------------------- scale and store
         pdl_wait();

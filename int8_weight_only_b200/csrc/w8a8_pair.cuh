@@ -130,7 +130,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
     using GroupsSh = typename std::conditional<kGrouped, Groups, OneGroup>::type;
     __shared__ GroupsSh groups_sh;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // warp-uniform
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair0 = blockIdx.x >> 1, P = gridDim.x >> 1;
@@ -223,37 +223,52 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
         }
     } else if (warp == 1) {
         // ---------------------------------------------------- products
-        if (lane == 0 && rank == 0) {
+        // The whole warp walks the steps and one elected lane issues, so that
+        // addresses and descriptors stay in uniform registers: with a branch
+        // on the lane number a product took 256 cycles to issue instead of
+        // the 128 it runs for (2048 x 4096 x 27392: 198 us).
+        if (rank == 0) {
             int st = 0, d = 0;
             uint32_t ph = 0, dph = 0;
             bool ok = true;
+            const uint64_t w_desc0 = smem_desc_kmajor_sw64(smem_u32(ring));
+            const uint64_t x_desc0 = smem_desc_kmajor_sw128(smem_u32(ring) + kWBytes);
             Sched<kGrouped> sched(p, groups, plan, pair0, P);
             Seg sg;
             while (ok && sched.next(sg)) {
                 int64_t row0;
                 const uint32_t idesc = idesc_u8_s8_s32(2 * kBN, width(rows_of(sg, row0)));
-                if (!mbar_wait(&d_empty[d], dph ^ 1u, SITE_I8_DEMPTY)) { ok = false; break; }
+                const uint32_t dst = tmem + d * kBT;
+                if (!warp_all(mbar_wait(&d_empty[d], dph ^ 1u, SITE_I8_DEMPTY))) { ok = false; break; }
                 tc_fence_after();
+                uint32_t acc = 0;
                 for (int ks = sg.ks0; ks < sg.ks1; ++ks) {
-                    const int cnt = min(kStepTiles, p.KB - kStepTiles * ks);
-                    if (!mbar_wait(&full[st], ph, SITE_I8_FULL)) { ok = false; break; }
+                    if (!warp_all(mbar_wait(&full[st], ph, SITE_I8_FULL))) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t wa = smem_u32(ring + st * kStageBytes), xa = wa + kWBytes;
-                    for (int t = 0; t < cnt; ++t) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            tc_mma_ss_i8_pair(tmem + d * kBT, smem_desc_kmajor_sw64(wa + t * kTile + 32 * j),
-                                              smem_desc_kmajor_sw128(xa + t * 64 + 32 * j), idesc,
-                                              ((ks - sg.ks0) | t | j) != 0);
+                    // descriptors count in units of 16 bytes; the sums stay
+                    // within the address field (shared memory < 256 KB)
+                    const uint64_t wd = w_desc0 + (uint32_t)st * (kStageBytes / 16);
+                    const uint64_t xd = x_desc0 + (uint32_t)st * (kStageBytes / 16);
+                    if (elect_one()) {
+                        tc_mma_ss_i8_pair(dst, wd, xd, idesc, acc);
+                        tc_mma_ss_i8_pair(dst, wd + 2, xd + 2, idesc, 1);
+                        if (kStepTiles * ks + 1 < p.KB) {
+                            tc_mma_ss_i8_pair(dst, wd + kTile / 16, xd + 4, idesc, 1);
+                            tc_mma_ss_i8_pair(dst, wd + kTile / 16 + 2, xd + 6, idesc, 1);
+                        }
+                        tc_commit_pair_mc(&empty[st], kBoth);
                     }
-                    tc_commit_pair_mc(&empty[st], kBoth);
+                    __syncwarp();
+                    acc = 1;
                     if (++st == kStages) { st = 0; ph ^= 1u; }
                 }
                 if (!ok) break;
-                tc_commit_pair_mc(&d_full[d], kBoth);
+                if (elect_one()) tc_commit_pair_mc(&d_full[d], kBoth);
+                __syncwarp();
                 if (++d == 2) { d = 0; dph ^= 1u; }
             }
-            tc_commit_pair(&drain);
+            if (elect_one()) tc_commit_pair(&drain);
+            __syncwarp();
             mbar_wait(&drain, 0, SITE_I8_DRAIN);
         }
     } else if (warp >= 4) {
