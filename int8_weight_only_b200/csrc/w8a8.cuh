@@ -144,6 +144,38 @@ struct Sched {
     }
 };
 
+// Scale and store the sums of C tokens (columns) of this thread's channel:
+// y points at the first token's output, rows of N apart; the first `left`
+// tokens exist.  sums and x_scales (shared memory, 16-byte aligned) belong to
+// the tokens.  All C tokens of existing channels in a straight line: with a
+// test at every store the scaling took longer than the products of a short
+// K (4096 x 768 x 2304: 24.6 us).
+template <int C>
+__device__ __forceinline__ void store_tokens(const uint32_t (&v)[C], const int *sums, const float *x_scales, int off,
+                                             float sc, float bi, uint16_t *y, int64_t N, int left) {
+    uint32_t h[C / 2];
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+        const int4 s4 = *reinterpret_cast<const int4 *>(sums + i);
+        const float4 x4 = *reinterpret_cast<const float4 *>(x_scales + i);
+        const float a = fmaf(__fmul_rn((float)((int)v[i] - off * s4.x), x4.x), sc, bi);
+        const float b = fmaf(__fmul_rn((float)((int)v[i + 1] - off * s4.y), x4.y), sc, bi);
+        const float c = fmaf(__fmul_rn((float)((int)v[i + 2] - off * s4.z), x4.z), sc, bi);
+        const float d = fmaf(__fmul_rn((float)((int)v[i + 3] - off * s4.w), x4.w), sc, bi);
+        const __half2 ab = __floats2half2_rn(a, b), cd = __floats2half2_rn(c, d);
+        h[i / 2] = *reinterpret_cast<const uint32_t *>(&ab);
+        h[i / 2 + 1] = *reinterpret_cast<const uint32_t *>(&cd);
+    }
+    if (left >= C) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) y[i * N] = (uint16_t)(i & 1 ? h[i / 2] >> 16 : h[i / 2]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (i < left) y[i * N] = (uint16_t)(i & 1 ? h[i / 2] >> 16 : h[i / 2]);
+    }
+}
+
 template <int TN, bool kGrouped>
 __global__ void __launch_bounds__(kThreads, 1)
 w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ Params p) {
@@ -316,22 +348,8 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
                 xs_sh[d][c] = c < nr ? __ldg(p.x_scales + row0 + c) : 0.0f;
             }
             uint16_t *const y0 = p.Y + row0 * p.N + n;
-            // scale 16 tokens' sums and store them
             auto store16 = [&](const uint32_t (&v)[16], int c0) {
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const int4 sm = *reinterpret_cast<const int4 *>(&sum_sh[d][c0 + i]);
-                    const float4 xs = *reinterpret_cast<const float4 *>(&xs_sh[d][c0 + i]);
-                    const int s4[4] = {sm.x, sm.y, sm.z, sm.w};
-                    const float x4[4] = {xs.x, xs.y, xs.z, xs.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int acc = (int)v[i + j] - off * s4[j];
-                        const float y = fmaf(__fmul_rn((float)acc, x4[j]), sc, bi);
-                        if (n_ok && c0 + i + j < nr)
-                            y0[(int64_t)(c0 + i + j) * p.N] = __half_as_ushort(__float2half_rn(y));
-                    }
-                }
+                store_tokens(v, &sum_sh[d][c0], &xs_sh[d][c0], off, sc, bi, y0 + c0 * p.N, p.N, n_ok ? nr - c0 : 0);
             };
             // all four warps give up together: they meet at barriers below
             // (this one also shows them the sums and scales)

@@ -297,20 +297,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
             }
             uint16_t *const y0 = p.Y + row0 * p.N + n;
             auto store32 = [&](const uint32_t (&v)[32], int c0) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const int4 sm = *reinterpret_cast<const int4 *>(&sum_sh[d][c0 + i]);
-                    const float4 xs = *reinterpret_cast<const float4 *>(&xs_sh[d][c0 + i]);
-                    const int s4[4] = {sm.x, sm.y, sm.z, sm.w};
-                    const float x4[4] = {xs.x, xs.y, xs.z, xs.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int acc = (int)v[i + j] - off * s4[j];
-                        const float y = fmaf(__fmul_rn((float)acc, x4[j]), sc, bi);
-                        if (n_ok && c0 + i + j < nr)
-                            y0[(int64_t)(c0 + i + j) * p.N] = __half_as_ushort(__float2half_rn(y));
-                    }
-                }
+                store_tokens(v, &sum_sh[d][c0], &xs_sh[d][c0], off, sc, bi, y0 + c0 * p.N, p.N, n_ok ? nr - c0 : 0);
             };
             if (!named_bar_all(1, 32 * kEpiWarps, mbar_wait(&d_full[d], dph, SITE_I8_DFULL))) break;
             tc_fence_after();
