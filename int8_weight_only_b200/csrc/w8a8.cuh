@@ -144,28 +144,36 @@ struct Sched {
     }
 };
 
-// Scale and store the sums of C tokens (columns) of this thread's channel:
-// y points at the first token's output, rows of N apart; the first `left`
-// tokens exist.  sums and x_scales (shared memory, 16-byte aligned) belong to
-// the tokens.  All C tokens of existing channels in a straight line: with a
-// test at every store the scaling took longer than the products of a short
-// K (4096 x 768 x 2304: 24.6 us).
+// The outputs of C tokens (columns) of this thread's channel, as pairs of
+// tokens: y = s_m s_n (sum - off sum_m) + bias, rounded once to fp16.  sums
+// and x_scales (shared memory, 16-byte aligned) belong to the tokens.
+template <int C>
+__device__ __forceinline__ void scale_tokens(const uint32_t (&v)[C], const int *sums, const float *x_scales, int off,
+                                             float sc, float bi, uint32_t (&h)[C / 2]) {
+    const uint64_t sc2 = f32x2(sc, sc), bi2 = f32x2(bi, bi);
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+        const int4 s4 = *reinterpret_cast<const int4 *>(sums + i);
+        const ulonglong2 x4 = *reinterpret_cast<const ulonglong2 *>(x_scales + i);
+        const uint64_t ab = f32x2((float)((int)v[i] - off * s4.x), (float)((int)v[i + 1] - off * s4.y));
+        const uint64_t cd = f32x2((float)((int)v[i + 2] - off * s4.z), (float)((int)v[i + 3] - off * s4.w));
+        const float2 y0 = f32x2_parts(f32x2_fma(f32x2_mul(ab, x4.x), sc2, bi2));
+        const float2 y1 = f32x2_parts(f32x2_fma(f32x2_mul(cd, x4.y), sc2, bi2));
+        const __half2 h0 = __float22half2_rn(y0), h1 = __float22half2_rn(y1);
+        h[i / 2] = *reinterpret_cast<const uint32_t *>(&h0);
+        h[i / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+    }
+}
+
+// Scale and store: y points at the first token's output of this channel,
+// rows of N apart; the first `left` tokens exist.  Whole runs of C tokens go
+// in a straight line: with a test at every store the scaling took longer than
+// the products of a short K.
 template <int C>
 __device__ __forceinline__ void store_tokens(const uint32_t (&v)[C], const int *sums, const float *x_scales, int off,
                                              float sc, float bi, uint16_t *y, int64_t N, int left) {
     uint32_t h[C / 2];
-#pragma unroll
-    for (int i = 0; i < C; i += 4) {
-        const int4 s4 = *reinterpret_cast<const int4 *>(sums + i);
-        const float4 x4 = *reinterpret_cast<const float4 *>(x_scales + i);
-        const float a = fmaf(__fmul_rn((float)((int)v[i] - off * s4.x), x4.x), sc, bi);
-        const float b = fmaf(__fmul_rn((float)((int)v[i + 1] - off * s4.y), x4.y), sc, bi);
-        const float c = fmaf(__fmul_rn((float)((int)v[i + 2] - off * s4.z), x4.z), sc, bi);
-        const float d = fmaf(__fmul_rn((float)((int)v[i + 3] - off * s4.w), x4.w), sc, bi);
-        const __half2 ab = __floats2half2_rn(a, b), cd = __floats2half2_rn(c, d);
-        h[i / 2] = *reinterpret_cast<const uint32_t *>(&ab);
-        h[i / 2 + 1] = *reinterpret_cast<const uint32_t *>(&cd);
-    }
+    scale_tokens(v, sums, x_scales, off, sc, bi, h);
     if (left >= C) {
 #pragma unroll
         for (int i = 0; i < C; ++i) y[i * N] = (uint16_t)(i & 1 ? h[i / 2] >> 16 : h[i / 2]);

@@ -25,12 +25,19 @@ constexpr int kStepTiles = 2;                // weight tiles per stage (128 feat
 constexpr int kWBytes = kStepTiles * kTile;
 constexpr int kXBytes = (kBT / 2) * 128;     // 128 tokens x 128 features
 constexpr int kStageBytes = kWBytes + kXBytes;
-constexpr int kStages = 6;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+constexpr int kStages = 5;
 constexpr int kEpiWarps = 8;
+constexpr int kParts = kEpiWarps / 4;        // a warp reads 32 of the 128 channels, of one part of the tokens
+constexpr int kPartTokens = kBT / kParts;
+// Outputs on their way out, per part two buffers of kChunk tokens x 128
+// channels fp16; the 16-byte piece c of token t lies at piece c ^ (t & 7).
+constexpr int kChunk = 32;
+constexpr int kOutBuf = kChunk * kBN * 2;
+constexpr int kOutBytes = kParts * 2 * kOutBuf;
+constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kTmemCols = 2 * kBT;
-constexpr int kPart = kBT * kBN;             // 32-bit sums of one block's share of a tile
+constexpr int kPartSums = kBT * kBN;             // 32-bit sums of one block's share of a tile
 constexpr uint16_t kBoth = 0x3;
 // K steps per pair that splitting the last tiles has to save
 constexpr int kSplitMin = 12;
@@ -121,6 +128,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *out_sh = ring + kStages * kStageBytes;
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ uint64_t d_full[2], d_empty[2], drain;
     __shared__ uint32_t tmem_base_sh;
@@ -275,43 +283,117 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
         // ---------------------------------------------------- scale and store
         pdl_wait();
         const int q4 = warp & 3;
-        const int half = (warp - 4) >> 2;     // token columns [128 half, 128 half + 128)
-        const int r = 32 * q4 + lane;
-        int d = 0;
+        const int part = (warp - 4) >> 2;     // token columns [kPartTokens part, + kPartTokens)
+        // Sums come as fragments: this thread holds channels ch0 + 8 j of the
+        // block, j < 4, and tokens 8 i + t0, + 1 of a chunk, i < 4.
+        const int ch0 = 32 * q4 + (lane >> 2);
+        const int t0 = 2 * (lane & 3);
+        int d = 0, buffer = 0;
         uint32_t dph = 0;
         Sched<kGrouped> sched(p, groups, plan, pair0, P);
-        Seg sg;
-        while (sched.next(sg)) {
+        // What the scaling of a tile reads from global memory: its channels'
+        // scales, biases and zero points and one token's scale and sum.
+        // Loaded a tile ahead, since a tile of short K is over before the
+        // loads are.
+        struct Operands {
+            Seg sg;
             int64_t row0;
-            const int nr = rows_of(sg, row0);
-            const int64_t n = (int64_t)(2 * sg.nbp + rank) * kBN + r;
-            const bool n_ok = n < p.N;
-            const int64_t ch = (int64_t)sg.group * p.N + n;
-            const float sc = n_ok ? __half2float(__ushort_as_half(p.scales[ch])) : 0.0f;
-            const float bi = (n_ok && p.bias) ? __half2float(__ushort_as_half(p.bias[ch])) : 0.0f;
-            const int off = 128 + ((n_ok && p.zeros) ? (int)p.zeros[ch] : 0);
-            {
-                const int c = threadIdx.x - 128;
-                sum_sh[d][c] = c < nr ? __ldg(p.x_sums + row0 + c) : 0;
-                xs_sh[d][c] = c < nr ? __ldg(p.x_scales + row0 + c) : 0.0f;
+            int nr;
+            uint16_t sc[4], bi[4];
+            int8_t z[4];
+            int sum;
+            float xs;
+        };
+        const int c_own = threadIdx.x - 128;     // this thread's token of the tile
+        auto fetch = [&](Operands &o) -> bool {
+            if (!sched.next(o.sg)) return false;
+            o.nr = rows_of(o.sg, o.row0);
+            const int64_t n0 = (int64_t)(2 * o.sg.nbp + rank) * kBN + ch0;
+            const int64_t at = (int64_t)o.sg.group * p.N + n0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool ok = n0 + 8 * j < p.N;
+                o.sc[j] = ok ? p.scales[at + 8 * j] : (uint16_t)0;
+                o.bi[j] = ok && p.bias ? p.bias[at + 8 * j] : (uint16_t)0;
+                o.z[j] = ok && p.zeros ? p.zeros[at + 8 * j] : (int8_t)0;
             }
-            uint16_t *const y0 = p.Y + row0 * p.N + n;
-            auto store32 = [&](const uint32_t (&v)[32], int c0) {
-                store_tokens(v, &sum_sh[d][c0], &xs_sh[d][c0], off, sc, bi, y0 + c0 * p.N, p.N, n_ok ? nr - c0 : 0);
+            o.sum = c_own < o.nr ? __ldg(p.x_sums + o.row0 + c_own) : 0;
+            o.xs = c_own < o.nr ? __ldg(p.x_scales + o.row0 + c_own) : 0.0f;
+            return true;
+        };
+        Operands next;
+        bool more = fetch(next);
+        while (more) {
+            const Seg sg = next.sg;
+            const int nr = next.nr;
+            uint64_t sc2[4], bi2[4];
+            int off[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float sc = __half2float(__ushort_as_half(next.sc[j])), bi = __half2float(__ushort_as_half(next.bi[j]));
+                sc2[j] = f32x2(sc, sc);
+                bi2[j] = f32x2(bi, bi);
+                off[j] = 128 + (int)next.z[j];
+            }
+            if (c_own < kBT) {
+                sum_sh[d][c_own] = next.sum;
+                xs_sh[d][c_own] = next.xs;
+            }
+            // kChunk tokens from column c0 leave through shared memory as
+            // whole rows of 128 channels, 16 bytes a lane.  The four warps of
+            // a part meet once a chunk: a buffer is refilled only after the
+            // barrier that every warp passes after reading it.
+            const int64_t nb0 = (int64_t)(2 * sg.nbp + rank) * kBN;
+            uint16_t *const y0 = p.Y + next.row0 * p.N + nb0 + 8 * (lane & 15);
+            const bool piece_ok = nb0 + 8 * (lane & 15) < p.N;
+            more = fetch(next);
+            auto store = [&](const uint32_t (&v)[kChunk], int c0) {
+                uint8_t *buf = out_sh + (2 * part + buffer) * kOutBuf;
+                buffer ^= 1;
+                // row of 16 bytes that this thread addresses: token lane % 8
+                // of a group of eight, piece lane / 8 of this warp's four
+                const uint32_t row = smem_u32(buf) + (lane & 7) * (kBN * 2) + (((4 * q4 + (lane >> 3)) ^ (lane & 7)) << 4);
+#pragma unroll
+                for (int i = 0; i < kChunk / 8; ++i) {
+                    const int2 s = *reinterpret_cast<const int2 *>(&sum_sh[d][c0 + 8 * i + t0]);
+                    const uint64_t x2 = *reinterpret_cast<const uint64_t *>(&xs_sh[d][c0 + 8 * i + t0]);
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int e = 16 * (j >> 1) + 4 * i + 2 * (j & 1);
+                        const uint64_t a = f32x2((float)((int)v[e] - off[j] * s.x), (float)((int)v[e + 1] - off[j] * s.y));
+                        const __half2 y = __float22half2_rn(f32x2_parts(f32x2_fma(f32x2_mul(a, x2), sc2[j], bi2[j])));
+                        h[j] = *reinterpret_cast<const uint32_t *>(&y);
+                    }
+                    stmatrix_x4_trans(row + i * 8 * (kBN * 2), h[0], h[1], h[2], h[3]);
+                }
+                named_bar_sync(2 + part, 128);
+#pragma unroll
+                for (int i = 0; i < kChunk / 8; ++i) {
+                    const int t = 8 * i + 2 * q4 + (lane >> 4);      // this half warp's token
+                    const uint4 w = *reinterpret_cast<const uint4 *>(buf + t * (kBN * 2) + (((lane & 15) ^ (t & 7)) << 4));
+                    if (piece_ok && c0 + t < nr) *reinterpret_cast<uint4 *>(y0 + (c0 + t) * p.N) = w;
+                }
             };
             if (!named_bar_all(1, 32 * kEpiWarps, mbar_wait(&d_full[d], dph, SITE_I8_DFULL))) break;
             tc_fence_after();
             const uint32_t src = tmem + ((uint32_t)(32 * q4) << 16) + d * kBT;
-            const int c_end = min(nr, 128 * half + 128);
-            int32_t *const mine = sg.slot < 0 ? nullptr : p.partials + ((int64_t)(pair0 * 2 + sg.slot) * 2 + rank) * kPart + r;
-            for (int c0 = 128 * half; c0 < c_end; c0 += 32) {
-                uint32_t v[32];
-                tmem_load_32(src + c0, v);
+            const int c_end = min(nr, kPartTokens * (part + 1));
+            // parts are kept as each thread holds them: [32 sums of a chunk][thread]
+            auto part_at = [&](int j, int slot, int c0) {
+                return p.partials + ((int64_t)(j * 2 + slot) * 2 + rank) * kPartSums +
+                       (c0 - kPartTokens * part) * (32 * kEpiWarps) + c_own;
+            };
+            for (int c0 = kPartTokens * part; c0 < c_end; c0 += kChunk) {
+                uint32_t v[kChunk];
+                tmem_load_frag_16x32(src + c0, v);
+                tmem_load_frag_16x32(src + (16u << 16) + c0, v + 16);
                 if (sg.slot < 0) {
-                    store32(v, c0);
+                    store(v, c0);
                 } else {
+                    int32_t *const mine = part_at(pair0, sg.slot, c0);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) __stcg(mine + (c0 + i) * kBN, (int32_t)v[i]);
+                    for (int i = 0; i < kChunk; ++i) __stcg(mine + i * (32 * kEpiWarps), (int32_t)v[i]);
                 }
             }
             tc_fence_before();
@@ -329,17 +411,16 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
                 }
                 named_bar_sync(1, 32 * kEpiWarps);
                 if (last_sh) {
-                    for (int c0 = 128 * half; c0 < c_end; c0 += 32) {
-                        uint32_t v[32];
+                    for (int c0 = kPartTokens * part; c0 < c_end; c0 += kChunk) {
+                        uint32_t v[kChunk];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0;
+                        for (int i = 0; i < kChunk; ++i) v[i] = 0;
                         for (int j = j0; j <= j1; ++j) {
-                            const int32_t *part =
-                                p.partials + ((int64_t)(j * 2 + plan.slot(j, sg.tile, KS)) * 2 + rank) * kPart + r;
+                            const int32_t *const theirs = part_at(j, plan.slot(j, sg.tile, KS), c0);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] += (uint32_t)__ldcg(part + (c0 + i) * kBN);
+                            for (int i = 0; i < kChunk; ++i) v[i] += (uint32_t)__ldcg(theirs + i * (32 * kEpiWarps));
                         }
-                        store32(v, c0);
+                        store(v, c0);
                     }
                 }
                 named_bar_sync(1, 32 * kEpiWarps);   // last_sh is read by all
