@@ -29,11 +29,11 @@ constexpr int kStages = 5;
 constexpr int kEpiWarps = 8;
 constexpr int kParts = kEpiWarps / 4;        // a warp reads 32 of the 128 channels, of one part of the tokens
 constexpr int kPartTokens = kBT / kParts;
-// Outputs on their way out, per part two buffers of kChunk tokens x 128
-// channels fp16; the 16-byte piece c of token t lies at piece c ^ (t & 7).
+// Outputs on their way out, per warp two buffers of kChunk tokens x its 32
+// channels fp16; the 16-byte piece c of token t lies at piece c ^ (t / 2 & 3).
 constexpr int kChunk = 32;
-constexpr int kOutBuf = kChunk * kBN * 2;
-constexpr int kOutBytes = kParts * 2 * kOutBuf;
+constexpr int kOutBuf = kChunk * 32 * 2;
+constexpr int kOutBytes = kEpiWarps * 2 * kOutBuf;
 constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kTmemCols = 2 * kBT;
@@ -339,40 +339,49 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
                 sum_sh[d][c_own] = next.sum;
                 xs_sh[d][c_own] = next.xs;
             }
-            // kChunk tokens from column c0 leave through shared memory as
-            // whole rows of 128 channels, 16 bytes a lane.  The four warps of
-            // a part meet once a chunk: a buffer is refilled only after the
-            // barrier that every warp passes after reading it.
-            const int64_t nb0 = (int64_t)(2 * sg.nbp + rank) * kBN;
-            uint16_t *const y0 = p.Y + next.row0 * p.N + nb0 + 8 * (lane & 15);
-            const bool piece_ok = nb0 + 8 * (lane & 15) < p.N;
+            // kChunk tokens from column c0 leave through this warp's part of
+            // shared memory as runs of its 32 channels, 16 bytes a lane.
+            // (Whole rows of 128 channels need a barrier of four warps a
+            // chunk, which cost more than the longer runs gave: 0.2 us.)
+            const int64_t n0 = (int64_t)(2 * sg.nbp + rank) * kBN + 32 * q4 + 8 * (lane & 3);
+            uint16_t *const y0 = p.Y + next.row0 * p.N + n0;
+            const bool piece_ok = n0 < p.N;
             more = fetch(next);
             auto store = [&](const uint32_t (&v)[kChunk], int c0) {
-                uint8_t *buf = out_sh + (2 * part + buffer) * kOutBuf;
+                uint8_t *buf = out_sh + (2 * (warp - 4) + buffer) * kOutBuf;
                 buffer ^= 1;
-                // row of 16 bytes that this thread addresses: token lane % 8
-                // of a group of eight, piece lane / 8 of this warp's four
-                const uint32_t row = smem_u32(buf) + (lane & 7) * (kBN * 2) + (((4 * q4 + (lane >> 3)) ^ (lane & 7)) << 4);
+                int2 s[kChunk / 8];
+                uint64_t x2[kChunk / 8];
 #pragma unroll
                 for (int i = 0; i < kChunk / 8; ++i) {
-                    const int2 s = *reinterpret_cast<const int2 *>(&sum_sh[d][c0 + 8 * i + t0]);
-                    const uint64_t x2 = *reinterpret_cast<const uint64_t *>(&xs_sh[d][c0 + 8 * i + t0]);
+                    s[i] = *reinterpret_cast<const int2 *>(&sum_sh[d][c0 + 8 * i + t0]);
+                    x2[i] = *reinterpret_cast<const uint64_t *>(&xs_sh[d][c0 + 8 * i + t0]);
+                }
+                // row of 16 bytes that this thread addresses: token lane % 8
+                // of a group of eight, piece lane / 8
+                const uint32_t row = smem_u32(buf) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+#pragma unroll
+                for (int i = 0; i < kChunk / 8; ++i) {
                     uint32_t h[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int e = 16 * (j >> 1) + 4 * i + 2 * (j & 1);
-                        const uint64_t a = f32x2((float)((int)v[e] - off[j] * s.x), (float)((int)v[e + 1] - off[j] * s.y));
-                        const __half2 y = __float22half2_rn(f32x2_parts(f32x2_fma(f32x2_mul(a, x2), sc2[j], bi2[j])));
+                        const uint64_t a = f32x2((float)((int)v[e] - off[j] * s[i].x), (float)((int)v[e + 1] - off[j] * s[i].y));
+                        const __half2 y = __float22half2_rn(f32x2_parts(f32x2_fma(f32x2_mul(a, x2[i]), sc2[j], bi2[j])));
                         h[j] = *reinterpret_cast<const uint32_t *>(&y);
                     }
-                    stmatrix_x4_trans(row + i * 8 * (kBN * 2), h[0], h[1], h[2], h[3]);
+                    stmatrix_x4_trans(row + i * 8 * 64, h[0], h[1], h[2], h[3]);
                 }
-                named_bar_sync(2 + part, 128);
+                __syncwarp();
+                uint4 w[kChunk / 8];
+#pragma unroll
+                for (int i = 0; i < kChunk / 8; ++i)
+                    w[i] = *reinterpret_cast<const uint4 *>(buf + i * 8 * 64 + (lane >> 2) * 64 +
+                                                            (((lane & 3) ^ ((lane >> 3) & 3)) << 4));
 #pragma unroll
                 for (int i = 0; i < kChunk / 8; ++i) {
-                    const int t = 8 * i + 2 * q4 + (lane >> 4);      // this half warp's token
-                    const uint4 w = *reinterpret_cast<const uint4 *>(buf + t * (kBN * 2) + (((lane & 15) ^ (t & 7)) << 4));
-                    if (piece_ok && c0 + t < nr) *reinterpret_cast<uint4 *>(y0 + (c0 + t) * p.N) = w;
+                    const int t = c0 + 8 * i + (lane >> 2);
+                    if (piece_ok && t < nr) *reinterpret_cast<uint4 *>(y0 + t * p.N) = w[i];
                 }
             };
             if (!named_bar_all(1, 32 * kEpiWarps, mbar_wait(&d_full[d], dph, SITE_I8_DFULL))) break;
