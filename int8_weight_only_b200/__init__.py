@@ -490,14 +490,22 @@ def _pitch(K):
     return (K + 15) // 16 * 16
 
 
-def _call(fn, what, device, *args):
-    """fn(*args, current stream of device) with that device current."""
+def _raw_stream(device):
+    """The device's current stream as an integer, without building a Stream
+    object where torch allows it (2 us of a 10 us call)."""
     torch = _torch()
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device.index) if get is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _call(fn, what, device, stream, *args):
+    """fn(*args, stream) with `device` current."""
+    cuda = _torch().cuda
+    if cuda.current_device() == device.index:
+        rc = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with cuda.device(device):
+            rc = fn(*args, stream)
     if rc != 0:
         raise W8Error(rc, what)
 
@@ -505,7 +513,7 @@ def _call(fn, what, device, *args):
 _ws_need = {}
 
 
-def _w8a8_workspace(device, M, K, N, workspace):
+def _w8a8_workspace(device, stream, K, N, workspace):
     """The scratch of a linear_w8a8 call.  Without one from the caller: the
     stream's default buffer, or, while a graph is captured, memory of that
     graph (two graphs replayed at once must not share it) whose counters
@@ -515,12 +523,13 @@ def _w8a8_workspace(device, M, K, N, workspace):
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {device}")
         return workspace
-    need = _ws_need.get((device, N))
+    need = _ws_need.get((device.index, N))
     if need is None:
         with torch.cuda.device(device):
-            need = _ws_need[(device, N)] = int(load_library().w8a8_workspace_bytes(max(M, 1), K, N))
+            need = _ws_need[(device.index, N)] = int(load_library().w8a8_workspace_bytes(1, K, N))
     if not torch.cuda.is_current_stream_capturing():
-        return _workspace(device, need)
+        buf = _ws_cache.get((device.index, stream))
+        return buf if buf is not None and buf.numel() >= need else _workspace(device, need)
     sms = torch.cuda.get_device_properties(device).multi_processor_count
     counters = max((N + 127) // 128, 2 * sms) * 4
     workspace = torch.empty((need,), dtype=torch.uint8, device=device)
@@ -531,7 +540,9 @@ def _w8a8_workspace(device, M, K, N, workspace):
 def _token_outputs(M, K, device, q, scales, sums):
     torch = _torch()
     if q is None:
-        q = torch.empty((M, _pitch(K)), dtype=torch.int8, device=device)[:, :K]
+        q = torch.empty((M, _pitch(K)), dtype=torch.int8, device=device)
+        if K % 16:
+            q = q[:, :K]
     elif q.dtype != torch.int8 or q.shape != (M, K) or q.device != device:
         raise ValueError(f"q must be {(M, K)} int8 on {device}")
     ldq = _rows(q, "q") if M > 1 else _pitch(K)
@@ -566,8 +577,8 @@ def quantize_tokens(X, q=None, scales=None, sums=None):
     M, K = X.shape
     dev = X.device
     q, ldq, scales, sums = _token_outputs(M, K, dev, q, scales, sums)
-    _call(lib.w8_quantize_per_token, "w8_quantize_per_token", dev, X.data_ptr(), dt, ldx, M, K, q.data_ptr(), ldq,
-          scales.data_ptr(), sums.data_ptr())
+    _call(lib.w8_quantize_per_token, "w8_quantize_per_token", dev, _raw_stream(dev), X.data_ptr(), dt, ldx, M, K,
+          q.data_ptr(), ldq, scales.data_ptr(), sums.data_ptr())
     return q, scales, sums
 
 
@@ -583,8 +594,8 @@ def swiglu_quantize_tokens(H, q=None, scales=None, sums=None):
     M, K = H.shape[0], H.shape[1] // 2
     dev = H.device
     q, ldq, scales, sums = _token_outputs(M, K, dev, q, scales, sums)
-    _call(lib.w8_swiglu_quantize_per_token, "w8_swiglu_quantize_per_token", dev, H.data_ptr(), ldh, M, K, q.data_ptr(),
-          ldq, scales.data_ptr(), sums.data_ptr())
+    _call(lib.w8_swiglu_quantize_per_token, "w8_swiglu_quantize_per_token", dev, _raw_stream(dev), H.data_ptr(), ldh,
+          M, K, q.data_ptr(), ldq, scales.data_ptr(), sums.data_ptr())
     return q, scales, sums
 
 
@@ -622,8 +633,9 @@ def linear_w8a8(q, x_scales, x_sums, packed, scales, bias=None, zeros=None, out=
     lib = load_library()
     ldq, M, K, N, out = _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, ())
     dev = q.device
-    ws = _w8a8_workspace(dev, M, K, N, workspace)
-    _call(lib.w8a8_linear, "w8a8_linear", dev, q.data_ptr(), ldq, x_scales.data_ptr(), x_sums.data_ptr(),
+    stream = _raw_stream(dev)
+    ws = _w8a8_workspace(dev, stream, K, N, workspace)
+    _call(lib.w8a8_linear, "w8a8_linear", dev, stream, q.data_ptr(), ldq, x_scales.data_ptr(), x_sums.data_ptr(),
           packed.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
           None if bias is None else bias.data_ptr(), out.data_ptr(), M, K, N, ws.data_ptr(), ws.numel() * ws.element_size())
     return out
@@ -644,8 +656,9 @@ def linear_w8a8_grouped(q, x_scales, x_sums, offsets, packed, scales, bias=None,
     ldq, M, K, N, out = _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, (E,))
     dev = q.device
     _need(offsets, "offsets", torch.int32, (E + 1,), dev)
-    ws = _w8a8_workspace(dev, M, K, N, workspace)
-    _call(lib.w8a8_linear_grouped, "w8a8_linear_grouped", dev, q.data_ptr(), ldq, x_scales.data_ptr(),
+    stream = _raw_stream(dev)
+    ws = _w8a8_workspace(dev, stream, K, N, workspace)
+    _call(lib.w8a8_linear_grouped, "w8a8_linear_grouped", dev, stream, q.data_ptr(), ldq, x_scales.data_ptr(),
           x_sums.data_ptr(), offsets.data_ptr(), E, packed.data_ptr(), scales.data_ptr(),
           None if zeros is None else zeros.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(),
           M, K, N, ws.data_ptr(), ws.numel() * ws.element_size())
