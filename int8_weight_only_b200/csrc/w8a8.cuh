@@ -33,8 +33,7 @@ constexpr int kBN = 128;                 // channels of an output tile
 constexpr int kTile = 8192;              // packed weight tile, 128 x 64
 constexpr int kStep = 4;                 // weight tiles per stage (256 features)
 constexpr int kWBytes = kStep * kTile;
-constexpr int kThreads = 256;
-constexpr int kEpiWarps = 4;
+constexpr int kPrefetch = 16;            // weight tiles brought into L2 ahead of the previous kernel's end
 constexpr int kMaxGroups = 1024;
 
 template <int TN>
@@ -45,6 +44,12 @@ struct Cfg {
     static constexpr int kStages = TN <= 16 ? 6 : TN <= 32 ? 5 : TN <= 64 ? 4 : 3;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
     static constexpr uint32_t kTmemCols = 2 * TN < 32 ? 32 : 2 * TN;
+    // four warps read the 128 channels; from 64 tokens on two sets of them
+    // share the tokens
+    static constexpr int kEpiWarps = TN >= 64 ? 8 : 4;
+    static constexpr int kThreads = 128 + 32 * kEpiWarps;
+    static constexpr int kEpiTokens = TN / (kEpiWarps / 4);
+    static constexpr int kChunk = TN >= 32 ? 32 : 16;        // tokens scaled at a time
     static_assert(kXBox % 1024 == 0, "swizzle alignment");
     static_assert(kSmemBytes <= 217 * 1024, "shared memory budget");
 };
@@ -185,7 +190,7 @@ __device__ __forceinline__ void store_tokens(const uint32_t (&v)[C], const int *
 }
 
 template <int TN, bool kGrouped>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<TN>::kThreads, 1)
 w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ Params p) {
     using C = Cfg<TN>;
     extern __shared__ uint8_t smem_raw[];
@@ -209,7 +214,7 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&d_full[i], 1);
-            mbar_init(&d_empty[i], kEpiWarps);
+            mbar_init(&d_empty[i], C::kEpiWarps);
         }
         mbar_init(&drain, 1);
         fence_barrier_init();
@@ -224,7 +229,7 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
     int64_t items;
     if constexpr (kGrouped) {
         pdl_wait();
-        load_groups<TN, kThreads>(p, *reinterpret_cast<Groups *>(&groups_sh));
+        load_groups<TN, C::kThreads>(p, *reinterpret_cast<Groups *>(&groups_sh));
         groups = reinterpret_cast<const Groups *>(&groups_sh);
     }
     tc_fence_before();
@@ -252,6 +257,16 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
     if (warp == 0) {
         // ---------------------------------------------------- producer
         if (lane == 0) {
+            if constexpr (!kGrouped) {
+                // the first weights into L2 while the previous kernel ends
+                // (never stale there, whoever writes them)
+                const int64_t it0 = min64(blockIdx.x, G) * items / G;
+                if (blockIdx.x < G) {
+                    const int64_t tt_n = (p.rows + TN - 1) / TN, unit = it0 / p.KB, kb = it0 - unit * p.KB;
+                    const int64_t left = min64((blockIdx.x + 1) * items / G - it0, p.KB - kb);
+                    prefetch_l2(p.packed + (unit / tt_n * p.KB + kb) * kTile, (uint32_t)min64(left, kPrefetch) * kTile);
+                }
+            }
             pdl_wait();
             int st = 0, issued = 0;
             uint32_t ph = 0;
@@ -334,8 +349,10 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
     } else if (warp >= 4) {
         // ---------------------------------------------------- scale and store
         pdl_wait();
+        constexpr int kEpi = 32 * C::kEpiWarps, kChunk = C::kChunk;
         const int q4 = warp & 3;
         const int r = 32 * q4 + lane;
+        const int cb = C::kEpiTokens * ((warp - 4) >> 2);     // this warp's first token
         int d = 0;
         uint32_t dph = 0;
         Sched<TN, kGrouped> sched(p, groups, items, G);
@@ -351,68 +368,105 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
             const int off = 128 + ((n_ok && p.zeros) ? (int)p.zeros[ch] : 0);
             // the tokens' sums and scales, read while the products run; the
             // other buffer may still be read for the tile before
-            for (int c = threadIdx.x - 128; c < TN; c += 32 * kEpiWarps) {
+            if (const int c = threadIdx.x - 128; c < TN) {
                 sum_sh[d][c] = c < nr ? __ldg(p.x_sums + row0 + c) : 0;
                 xs_sh[d][c] = c < nr ? __ldg(p.x_scales + row0 + c) : 0.0f;
             }
             uint16_t *const y0 = p.Y + row0 * p.N + n;
-            auto store16 = [&](const uint32_t (&v)[16], int c0) {
+            auto store = [&](const uint32_t (&v)[kChunk], int c0) {
                 store_tokens(v, &sum_sh[d][c0], &xs_sh[d][c0], off, sc, bi, y0 + c0 * p.N, p.N, n_ok ? nr - c0 : 0);
             };
-            // all four warps give up together: they meet at barriers below
-            // (this one also shows them the sums and scales)
-            if (!named_bar_all(1, 32 * kEpiWarps, mbar_wait(&d_full[d], dph, SITE_I8_DFULL))) break;
-            tc_fence_after();
+            const int c_end = min(nr, cb + C::kEpiTokens);
             const uint32_t src = tmem + ((uint32_t)(32 * q4) << 16) + d * TN;
+            // A block's part of a shared output tile: [4 tokens][channel][4],
+            // 16 bytes a thread.  Slot 0 is of the tile that the block's run
+            // begins in, slot 1 of the one it ends in.
+            auto part_at = [&](int64_t j, int c0) {
+                const int64_t begin = j * items / G;
+                return reinterpret_cast<int4 *>(p.partials + (j * 2 + (begin / p.KB == sg.unit ? 0 : 1)) * (TN * kBN) +
+                                                c0 * kBN + 4 * r);
+            };
+            // blocks that share this output tile: the owners of its first to
+            // last weight tile; the first one's counter is the tile's
             const bool whole = sg.kb0 == 0 && sg.kb1 == p.KB;
-            int32_t *mine = nullptr;
+            int64_t j0 = 0, j1 = 0;
             if (!whole) {
-                const int64_t begin = (int64_t)blockIdx.x * items / G;
-                mine = p.partials + ((int64_t)blockIdx.x * 2 + (begin / p.KB == sg.unit ? 0 : 1)) * (TN * kBN) + r;
+                const int64_t it0 = sg.unit * p.KB;
+                j0 = ((it0 + 1) * G - 1) / items;
+                j1 = ((it0 + p.KB) * G - 1) / items;
             }
-            for (int c0 = 0; c0 < nr; c0 += 16) {
-                uint32_t v[16];
-                tmem_load_16(src + c0, v);
-                if (whole) {
-                    store16(v, c0);
-                } else {
+            int *const cnt = p.counters + j0;
+            // all epilogue warps give up together: they meet at barriers
+            // below (this one also shows them the sums and scales)
+            if (!named_bar_all(1, kEpi, mbar_wait(&d_full[d], dph, SITE_I8_DFULL))) break;
+            tc_fence_after();
+            // The block that a tile begins in ends its run with it; the
+            // others often had theirs done long before, at the start of
+            // their runs.  Then it finishes the tile from tensor memory and
+            // stores no part of its own.
+            bool finish = whole;
+            if (!whole && sg.kb0 == 0) {
+                if (threadIdx.x == 128) {
+                    const int all = ld_acquire_gpu(cnt) == (int)(j1 - j0);
+                    if (all) *cnt = 0;
+                    last_sh = all;
+                }
+                named_bar_sync(1, kEpi);
+                finish = last_sh;
+            }
+            if (!finish) {
+                for (int c0 = cb; c0 < c_end; c0 += kChunk) {
+                    uint32_t v[kChunk];
+                    if constexpr (kChunk == 32) tmem_load_32(src + c0, v); else tmem_load_16(src + c0, v);
+                    int4 *const mine = part_at(blockIdx.x, c0);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) __stcg(mine + (c0 + i) * kBN, (int32_t)v[i]);
+                    for (int i = 0; i < kChunk / 4; ++i)
+                        __stcg(mine + i * kBN, make_int4((int)v[4 * i], (int)v[4 * i + 1], (int)v[4 * i + 2], (int)v[4 * i + 3]));
+                }
+                named_bar_sync(1, kEpi);   // the part is written (and last_sh read)
+                if (threadIdx.x == 128) {
+                    const int last = atomic_add_acq_rel_gpu(cnt, 1) == (int)(j1 - j0);
+                    if (last) *cnt = 0;
+                    last_sh = last;
+                }
+                named_bar_sync(1, kEpi);
+                finish = last_sh;
+            }
+            if (finish) {
+                for (int c0 = cb; c0 < c_end; c0 += kChunk) {
+                    uint32_t v[kChunk];
+                    if constexpr (kChunk == 32) tmem_load_32(src + c0, v); else tmem_load_16(src + c0, v);
+                    if (!whole) {
+                        // the others' parts, several blocks' loads in flight
+                        constexpr int kAhead = TN >= 64 ? 2 : TN == 32 ? 3 : 6;
+                        for (int64_t j = j0; j <= j1; j += kAhead) {
+                            int4 t[kAhead][kChunk / 4];
+#pragma unroll
+                            for (int a = 0; a < kAhead; ++a) {
+                                const bool there = j + a <= j1 && j + a != blockIdx.x;
+                                const int4 *const theirs = part_at(there ? j + a : j0, c0);
+#pragma unroll
+                                for (int i = 0; i < kChunk / 4; ++i)
+                                    t[a][i] = there ? __ldcg(theirs + i * kBN) : make_int4(0, 0, 0, 0);
+                            }
+#pragma unroll
+                            for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+                                for (int i = 0; i < kChunk / 4; ++i) {
+                                    v[4 * i] += (uint32_t)t[a][i].x;
+                                    v[4 * i + 1] += (uint32_t)t[a][i].y;
+                                    v[4 * i + 2] += (uint32_t)t[a][i].z;
+                                    v[4 * i + 3] += (uint32_t)t[a][i].w;
+                                }
+                        }
+                    }
+                    store(v, c0);
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_empty[d]);
-            if (!whole) {
-                // blocks that share this output tile: the owners of its first
-                // to last weight tile; the first one's counter is the tile's
-                const int64_t it0 = sg.unit * p.KB;
-                const int64_t j0 = ((it0 + 1) * G - 1) / items, j1 = ((it0 + p.KB) * G - 1) / items;
-                named_bar_sync(1, 32 * kEpiWarps);   // the part is written
-                if (threadIdx.x == 128) {
-                    const int have = atomic_add_acq_rel_gpu(p.counters + j0, 1) + 1;
-                    const int last = have == (int)(j1 - j0) + 1;
-                    if (last) p.counters[j0] = 0;
-                    last_sh = last;
-                }
-                named_bar_sync(1, 32 * kEpiWarps);
-                if (last_sh) {
-                    for (int c0 = 0; c0 < nr; c0 += 16) {
-                        uint32_t v[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = 0;
-                        for (int64_t j = j0; j <= j1; ++j) {
-                            const int64_t begin = j * items / G;
-                            const int32_t *part =
-                                p.partials + (j * 2 + (begin / p.KB == sg.unit ? 0 : 1)) * (TN * kBN) + r;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] += (uint32_t)__ldcg(part + (c0 + i) * kBN);
-                        }
-                        store16(v, c0);
-                    }
-                }
-                named_bar_sync(1, 32 * kEpiWarps);   // last_sh is read by all
-            }
+            if (!whole) named_bar_sync(1, kEpi);   // last_sh is read by all
             if (++d == 2) { d = 0; dph ^= 1u; }
         }
     }

@@ -97,7 +97,7 @@ int launch_w8a8_as(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const
     // the two shared output tiles of each
     const int64_t slots = (int64_t)(partial_area_bytes(d->sms) / (2 * (size_t)TN * w8a8::kBN * sizeof(int32_t)));
     cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(d->sms, slots)), 1, 1);
-    cfg.blockDim = dim3(w8a8::kThreads, 1, 1);
+    cfg.blockDim = dim3(w8a8::Cfg<TN>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = w8a8::Cfg<TN>::kSmemBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
