@@ -33,7 +33,15 @@ constexpr int kBN = 128;                 // channels of an output tile
 constexpr int kTile = 8192;              // packed weight tile, 128 x 64
 constexpr int kStep = 4;                 // weight tiles per stage (256 features)
 constexpr int kWBytes = kStep * kTile;
-constexpr int kPrefetch = 16;            // weight tiles brought into L2 ahead of the previous kernel's end
+// Weight tiles that a block gets at least, unless output tiles would then
+// share a block: sharing an output tile costs 2-3 us, a run of 16 tiles 1.5 us
+// (1 x 1024 x 1024: 9.9 us with runs of one tile, 6.0 with 4, 4.2 with 16;
+// 128 x 2048 x 2048: 17.9, 15.1, 10.0, and 7.3 with 32).
+constexpr int kMinRun = 32;
+// Weight tiles that a block brings into L2 ahead of the previous kernel's end
+// (1 x 4096 x 27392: 23.6 us with 1, 21.9 with 16, 21.6 with 32; 4 stages of
+// 256 features: 6 stages take 1 us more).
+constexpr int kPrefetch = 32;
 constexpr int kMaxGroups = 1024;
 
 template <int TN>
@@ -41,7 +49,7 @@ struct Cfg {
     static constexpr int kXBox = TN * 128;                   // TN tokens x 128 features
     static constexpr int kXBytes = (kStep / 2) * kXBox;
     static constexpr int kStageBytes = kWBytes + kXBytes;
-    static constexpr int kStages = TN <= 16 ? 6 : TN <= 32 ? 5 : TN <= 64 ? 4 : 3;
+    static constexpr int kStages = TN <= 64 ? 4 : 3;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
     static constexpr uint32_t kTmemCols = 2 * TN < 32 ? 32 : 2 * TN;
     // four warps read the 128 channels; from 64 tokens on two sets of them
@@ -83,7 +91,7 @@ struct OneGroup {};
 // first rows are clamped to [0, rows], so no offset can lead out of bounds.
 template <int TN, int kThreads_>
 __device__ __forceinline__ void load_groups(const Params &p, Groups &g) {
-    for (int e = threadIdx.x; e <= p.groups; e += kThreads_) g.first[e] = (int)max64(0, min64(p.rows, p.offsets[e]));
+    for (int e = threadIdx.x; e <= p.groups; e += kThreads_) g.first[e] = (int)max64(0, min64(p.rows, __ldcg(p.offsets + e)));
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
@@ -226,23 +234,45 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
     }
     pdl_launch_dependents();
     const Groups *groups = nullptr;
-    int64_t items;
+    if constexpr (kGrouped) groups = reinterpret_cast<const Groups *>(&groups_sh);
+    // the weight tiles of all output tiles
+    auto count = [&]() -> int64_t {
+        if constexpr (kGrouped)
+            return (int64_t)groups->tiles[p.groups] * p.NB * p.KB;
+        else
+            return (p.rows + TN - 1) / TN * p.NB * p.KB;
+    };
+    // blocks with work: every one of them has at least one weight tile, and
+    // kMinRun of them unless that would leave output tiles to share a block
+    auto blocks = [&](int64_t items) -> int64_t {
+        return max64(1, min64(gridDim.x, max64(items / p.KB, items / kMinRun)));
+    };
+    // The first weights into L2 while the previous kernel ends; they are never
+    // stale there, whoever writes them.  The offsets may still be written:
+    // here they are only a guess at what to bring, read past L1, and read
+    // again below.
+    if constexpr (kGrouped) {
+        load_groups<TN, C::kThreads>(p, *reinterpret_cast<Groups *>(&groups_sh));
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        const int64_t items = count();
+        Sched<TN, kGrouped> sched(p, groups, items, blocks(items));
+        Seg sg;
+        if (sched.next(sg))
+            prefetch_l2(p.packed + (((int64_t)sg.group * p.NB + sg.nb) * p.KB + sg.kb0) * kTile,
+                        (uint32_t)min(sg.kb1 - sg.kb0, kPrefetch) * kTile);
+    }
     if constexpr (kGrouped) {
         pdl_wait();
+        __syncthreads();   // the guess has been read
         load_groups<TN, C::kThreads>(p, *reinterpret_cast<Groups *>(&groups_sh));
-        groups = reinterpret_cast<const Groups *>(&groups_sh);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
-    if constexpr (kGrouped) {
-        items = (int64_t)groups->tiles[p.groups] * p.NB * p.KB;
-    } else {
-        items = (p.rows + TN - 1) / TN * p.NB * p.KB;
-    }
-    // blocks with work: every one of them has at least one weight tile
-    const int64_t G = max64(1, min64(gridDim.x, items));
+    const int64_t items = count(), G = blocks(items);
     // rows of a segment's token tile: the first, and how many of the group's
     auto rows_of = [&](const Seg &s, int64_t &row0) -> int {
         int64_t first = 0, end = p.rows;
@@ -257,16 +287,6 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
     if (warp == 0) {
         // ---------------------------------------------------- producer
         if (lane == 0) {
-            if constexpr (!kGrouped) {
-                // the first weights into L2 while the previous kernel ends
-                // (never stale there, whoever writes them)
-                const int64_t it0 = min64(blockIdx.x, G) * items / G;
-                if (blockIdx.x < G) {
-                    const int64_t tt_n = (p.rows + TN - 1) / TN, unit = it0 / p.KB, kb = it0 - unit * p.KB;
-                    const int64_t left = min64((blockIdx.x + 1) * items / G - it0, p.KB - kb);
-                    prefetch_l2(p.packed + (unit / tt_n * p.KB + kb) * kTile, (uint32_t)min64(left, kPrefetch) * kTile);
-                }
-            }
             pdl_wait();
             int st = 0, issued = 0;
             uint32_t ph = 0;

@@ -5,6 +5,7 @@
 
 #include "tokens.cuh"
 #include "w8a8.cuh"
+#include "w8a8_cluster.cuh"
 #include "w8a8_pair.cuh"
 
 namespace {
@@ -87,8 +88,74 @@ int make_map_codes(CUtensorMap *map, const int8_t *q, int64_t ldq, int64_t rows,
     return r == CUDA_SUCCESS ? W8_OK : W8_ERR_CUDA;
 }
 
+// Blocks of a cluster for few output tiles (w8a8_cluster.cuh), 0 where the
+// even split over all blocks serves better: the largest C whose clusters can
+// all run at once, with at least kClusterRun weight tiles for each block
+// (1 x 1024 x 1024: 2.9 us with 4, 3.2 with 8, 4.2 with 16; 100 x 1024 x 1024:
+// 5.0, 5.8, 5.7).
+constexpr int64_t kClusterRun = 4;
+template <int TN>
+int w8a8_cluster_size(DeviceInfo *d, int64_t units, int64_t KB) {
+    for (int c = w8a8::cluster::kMaxCluster; c >= 2; c >>= 1) {
+        if (units * c > d->sms || KB < (int64_t)c * kClusterRun) continue;
+        const void *fn = (const void *)w8a8::cluster::w8a8_cluster_kernel<TN>;
+        std::lock_guard<std::mutex> lock(g_mu);
+        int &cached = d->dclusters[{fn, c}];
+        if (cached == 0) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(d->sms / c * c), 1, 1);
+            cfg.blockDim = dim3(w8a8::cluster::Cfg<TN>::kThreads, 1, 1);
+            cfg.dynamicSmemBytes = w8a8::cluster::Cfg<TN>::kSmemBytes;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = c;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, w8a8::cluster::w8a8_cluster_kernel<TN>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            cached = n > 0 ? n : -1;
+        }
+        if (cached >= units) return c;
+    }
+    return 0;
+}
+
+template <int TN>
+int launch_w8a8_cluster(int c, int64_t units, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p,
+                        cudaStream_t st) {
+    CUtensorMap map;
+    const int rc = make_map_codes(&map, q, ldq, p.rows, K, TN);
+    if (rc != W8_OK) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * c), 1, 1);
+    cfg.blockDim = dim3(w8a8::cluster::Cfg<TN>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = w8a8::cluster::Cfg<TN>::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = c;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, w8a8::cluster::w8a8_cluster_kernel<TN>, map, p) != cudaSuccess) return cuda_fail();
+    return launch_status();
+}
+
 template <int TN, bool kGrouped>
 int launch_w8a8_as(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
+    if constexpr (!kGrouped) {
+        const int64_t units = cdiv(p.rows, TN) * p.NB;
+        const int c = w8a8_cluster_size<TN>(d, units, p.KB);
+        if (c > 0) return launch_w8a8_cluster<TN>(c, units, q, ldq, K, p, st);
+    }
     CUtensorMap map;
     const int rc = make_map_codes(&map, q, ldq, p.rows, K, TN);
     if (rc != W8_OK) return rc;
@@ -172,6 +239,15 @@ int launch_w8a8(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8
 
 cudaError_t w8a8_attributes() {
     cudaError_t e = cudaSuccess;
+#define W8_I8_CLUSTER_SMEM(TN)                                                                            \
+    if (e == cudaSuccess)                                                                                     \
+        e = cudaFuncSetAttribute((const void *)w8a8::cluster::w8a8_cluster_kernel<TN>,                       \
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, w8a8::cluster::Cfg<TN>::kSmemBytes);
+    W8_I8_CLUSTER_SMEM(16)
+    W8_I8_CLUSTER_SMEM(32)
+    W8_I8_CLUSTER_SMEM(64)
+    W8_I8_CLUSTER_SMEM(128)
+#undef W8_I8_CLUSTER_SMEM
 #define W8_I8_SMEM(TN)                                                                                        \
     for (const void *f : {(const void *)w8a8::w8a8_kernel<TN, false>, (const void *)w8a8::w8a8_kernel<TN, true>}) \
         if (e == cudaSuccess)                                                                                 \
