@@ -29,63 +29,140 @@ struct Params {
     int32_t *sums;
 };
 
-__device__ __forceinline__ void widen8(const uint4 &v, float (&f)[8]) {
+// Values travel as pairs of fp32 (f32x2): most steps below are IEEE operations
+// on two values at once, half the instructions of this kernel's bound.
+__device__ __forceinline__ void widen8(const uint4 &v, uint64_t (&f)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        f[2 * i] = p.x;
-        f[2 * i + 1] = p.y;
+        f[i] = f32x2(p.x, p.y);
+    }
+}
+
+// g / (1 + exp(-g)), every step correctly rounded: the values of an
+// elementwise formula in fp32.
+__device__ __forceinline__ float silu_ieee(float g) { return __fdiv_rn(g, __fadd_rn(1.0f, expf(-g))); }
+
+// The same for two values with |g| <= kSiluFast.  The quotient by Markstein's
+// method (IBM J. Res. Dev. 34(1), 1990): a reciprocal refined once, r, a
+// quotient q = g r and its exact remainder, q + (g - d q) r.  It gives the
+// correctly rounded quotient for every one of the fp16 gates, which
+// tests/test_tokens_gpu.py checks one by one against silu_ieee's values.
+constexpr float kSiluFast = 80.0f;
+__device__ __forceinline__ float rcp_approx(float d) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return r;
+}
+__device__ __forceinline__ uint64_t f32x2_neg(uint64_t a) { return a ^ 0x8000000080000000ull; }
+__device__ __forceinline__ uint64_t silu2(uint64_t g) {
+    const float2 v = f32x2_parts(g);
+    const uint64_t one = f32x2(1.0f, 1.0f);
+    const uint64_t d = f32x2_add(one, f32x2(expf(-v.x), expf(-v.y)));
+    const float2 dv = f32x2_parts(d);
+    const uint64_t nd = f32x2_neg(d);
+    uint64_t r = f32x2(rcp_approx(dv.x), rcp_approx(dv.y));
+    r = f32x2_fma(r, f32x2_fma(nd, r, one), r);
+    const uint64_t q = f32x2_mul(g, r);
+    return f32x2_fma(f32x2_fma(nd, q, g), r, q);
+}
+
+// Bits of the magnitudes of eight values, the largest of each of the four
+// words' halves together.
+__device__ __forceinline__ __half2 max_abs8(const uint4 &g) {
+    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+    __half2 m = __habs2(*reinterpret_cast<const __half2 *>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __half2 *>(&w[i])));
+    return m;
+}
+
+__device__ __forceinline__ void swiglu8(const uint4 &g, const uint4 &u, uint64_t (&f)[4]) {
+    uint64_t up[4];
+    widen8(g, f);
+    widen8(u, up);
+    // (false for NaN: those take the plain formula)
+    if (__hble2(max_abs8(g), __float2half2_rn(kSiluFast))) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = f32x2_mul(silu2(f[i]), up[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = f32x2_parts(f[i]);
+            f[i] = f32x2_mul(f32x2(silu_ieee(v.x), silu_ieee(v.y)), up[i]);
+        }
     }
 }
 
 // Eight consecutive values of a row, from element k.
 template <int kSrc>
-__device__ __forceinline__ void load8(const Params &p, int64_t row, int64_t k, float (&f)[8]) {
+__device__ __forceinline__ void load8(const Params &p, int64_t row, int64_t k, uint64_t (&f)[4]) {
     if constexpr (kSrc == kF32) {
-        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.X) + row * p.ldx + k);
-        const float4 a = __ldg(src), b = __ldg(src + 1);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        const ulonglong2 *src = reinterpret_cast<const ulonglong2 *>(static_cast<const float *>(p.X) + row * p.ldx + k);
+        const ulonglong2 a = __ldg(src), b = __ldg(src + 1);
+        f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+    } else if constexpr (kSrc == kF16) {
+        widen8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.X) + row * p.ldx + k)), f);
     } else {
         const uint16_t *src = static_cast<const uint16_t *>(p.X) + row * p.ldx + k;
-        widen8(__ldg(reinterpret_cast<const uint4 *>(src)), f);
-        if constexpr (kSrc == kSwiglu) {
-            float u[8];
-            widen8(__ldg(reinterpret_cast<const uint4 *>(src + p.K)), u);
-            // every step one IEEE operation: the same values as an
-            // elementwise formula in fp32
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(__fdiv_rn(f[i], 1.0f + expf(-f[i])), u[i]);
-        }
+        const uint4 g = __ldg(reinterpret_cast<const uint4 *>(src)), u = __ldg(reinterpret_cast<const uint4 *>(src + p.K));
+        swiglu8(g, u, f);
     }
 }
+
+// What the codes of a row need: its scale and 1 / scale.  A scale below
+// fp32's normal range has no usable reciprocal: NaN sends every value to the
+// IEEE quotient.
+struct RowScale {
+    float s, inv;
+    __device__ explicit RowScale(float amax) {
+        s = __fdiv_rn(amax, 127.0f);
+        inv = s >= 1.17549435e-38f ? __fdiv_rn(1.0f, s) : __int_as_float(0x7fffffff);
+    }
+};
 
 // The codes of eight values, as two words.  x / s is formed as x fl(1/s),
 // within 2^-15 of the quotient for |x / s| <= 128, and rounded by adding
 // 1.5 2^23; where the product lies within 2^-13 of a half-integer (or is not
-// finite) the IEEE quotient decides.
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float s, float inv) {
+// finite) the IEEE quotient decides.  (Elsewhere no code passes 127: the
+// largest value over a normal s is within 2^-16 of 127.)
+__device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], const RowScale &rs) {
     constexpr float kMagic = 12582912.0f;
-    float t[8];
-    bool near_half = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float r = __fmul_rn(f[i], inv);
-        t[i] = __fadd_rn(r, kMagic);
-        near_half |= !(fabsf(__fsub_rn(r, __fsub_rn(t[i], kMagic))) < 0.5f - 0x1p-13f);
-    }
-    if (near_half) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = __fadd_rn(fminf(fmaxf(__fdiv_rn(f[i], s), -127.0f), 127.0f), kMagic);
-    }
+    if (!(rs.s > 0.0f)) return make_uint2(0u, 0u);
+    const uint64_t magic = f32x2(kMagic, kMagic), inv = f32x2(rs.inv, rs.inv);
     uint32_t b[8];
+    bool safe = true;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fminf(fmaxf(t[i], kMagic - 127.0f), kMagic + 127.0f));
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t r = f32x2_mul(f[i], inv), t = f32x2_add(r, magic);
+        const float2 off = f32x2_parts(f32x2_sub(r, f32x2_sub(t, magic)));
+        safe = safe && fabsf(off.x) < 0.5f - 0x1p-13f && fabsf(off.y) < 0.5f - 0x1p-13f;
+        const float2 tv = f32x2_parts(t);
+        b[2 * i] = __float_as_uint(tv.x);
+        b[2 * i + 1] = __float_as_uint(tv.y);
+    }
+    if (!safe) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = f32x2_parts(f[i]);
+            b[2 * i] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(v.x, rs.s), -127.0f), 127.0f), kMagic));
+            b[2 * i + 1] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(v.y, rs.s), -127.0f), 127.0f), kMagic));
+        }
+    }
     uint2 out;
     out.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
     out.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
     return out;
+}
+
+__device__ __forceinline__ float max_abs(const uint64_t (&f)[4], float m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = f32x2_parts(f[i]);
+        m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+    }
+    return m;
 }
 
 template <int TPR>
@@ -134,55 +211,48 @@ __global__ void __launch_bounds__(kBlock<TPR>) quantize_tokens_kernel(const __gr
     int8_t *dst = p.q + row * p.ldq;
     int sum = 0;
     if constexpr (V > 0) {
-        float f[V][8];
+        uint64_t f[V][4];
 #pragma unroll
         for (int c = 0; c < V; ++c) {
             if (k0 + c * kStep < p.K) {
                 load8<kSrc>(p, row, k0 + c * kStep, f[c]);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[c][i] = 0.0f;
+                for (int i = 0; i < 4; ++i) f[c][i] = 0;
             }
         }
 #pragma unroll
-        for (int c = 0; c < V; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[c][i]));
-        amax = row_max<TPR>(amax, sh_max);
-        const float s = __fdiv_rn(amax, 127.0f);
-        const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+        for (int c = 0; c < V; ++c) amax = max_abs(f[c], amax);
+        const RowScale rs(row_max<TPR>(amax, sh_max));
 #pragma unroll
         for (int c = 0; c < V; ++c) {
             if (k0 + c * kStep < p.K) {
-                const uint2 w = s > 0.0f ? codes8(f[c], s, inv) : make_uint2(0u, 0u);
+                const uint2 w = codes8(f[c], rs);
                 *reinterpret_cast<uint2 *>(dst + k0 + c * kStep) = w;
                 sum = __dp4a((int)w.x, 0x01010101, __dp4a((int)w.y, 0x01010101, sum));
             }
         }
         sum = row_sum<TPR>(sum, sh_sum);
         if (k0 == 0) {
-            p.scales[row] = s;
+            p.scales[row] = rs.s;
             p.sums[row] = sum;
         }
     } else {
-        float f[8];
+        uint64_t f[4];
         for (int64_t k = k0; k < p.K; k += kStep) {
             load8<kSrc>(p, row, k, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+            amax = max_abs(f, amax);
         }
-        amax = row_max<TPR>(amax, sh_max);
-        const float s = __fdiv_rn(amax, 127.0f);
-        const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+        const RowScale rs(row_max<TPR>(amax, sh_max));
         for (int64_t k = k0; k < p.K; k += kStep) {
             load8<kSrc>(p, row, k, f);
-            const uint2 w = s > 0.0f ? codes8(f, s, inv) : make_uint2(0u, 0u);
+            const uint2 w = codes8(f, rs);
             *reinterpret_cast<uint2 *>(dst + k) = w;
             sum = __dp4a((int)w.x, 0x01010101, __dp4a((int)w.y, 0x01010101, sum));
         }
         sum = row_sum<TPR>(sum, sh_sum);
         if (k0 == 0) {
-            p.scales[row] = s;
+            p.scales[row] = rs.s;
             p.sums[row] = sum;
         }
     }

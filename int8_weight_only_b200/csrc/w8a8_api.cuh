@@ -38,12 +38,42 @@ int launch_tokens_as(const tokens::Params &p, cudaStream_t st) {
     return launch_status();
 }
 
+// A row by one warp up to 1024 elements, by 256 threads up to 16384 where
+// there are rows enough to fill the GPU, else by 512 (a row's latency counts);
+// longer rows are read twice.
 template <int kSrc>
-int launch_tokens(const tokens::Params &p, cudaStream_t st) {
-    if (p.K <= 512) return launch_tokens_as<kSrc, 32, 2>(p, st);
-    if (p.K <= 4096) return launch_tokens_as<kSrc, 256, 2>(p, st);
-    if (p.K <= 16384) return launch_tokens_as<kSrc, 512, 4>(p, st);
-    return launch_tokens_as<kSrc, 512, 0>(p, st);
+int launch_tokens(DeviceInfo *d, const tokens::Params &p, cudaStream_t st) {
+#ifndef W8_TOK_ROWS
+#define W8_TOK_ROWS 4
+#endif
+    const bool many = p.M > W8_TOK_ROWS * d->sms;
+    if (p.K <= 1024 && (many || p.K <= 256)) {
+        switch (cdiv(p.K, 256)) {
+            case 1: return launch_tokens_as<kSrc, 32, 1>(p, st);
+            case 2: return launch_tokens_as<kSrc, 32, 2>(p, st);
+            default: return launch_tokens_as<kSrc, 32, 4>(p, st);
+        }
+    }
+    if (many) {
+        switch (cdiv(p.K, 2048)) {
+            case 1: return launch_tokens_as<kSrc, 256, 1>(p, st);
+            case 2: return launch_tokens_as<kSrc, 256, 2>(p, st);
+            case 3: return launch_tokens_as<kSrc, 256, 3>(p, st);
+            case 4: return launch_tokens_as<kSrc, 256, 4>(p, st);
+            case 5: return launch_tokens_as<kSrc, 256, 5>(p, st);
+            case 6: return launch_tokens_as<kSrc, 256, 6>(p, st);
+            case 7: return launch_tokens_as<kSrc, 256, 7>(p, st);
+            case 8: return launch_tokens_as<kSrc, 256, 8>(p, st);
+            default: break;
+        }
+    }
+    switch (cdiv(p.K, 4096)) {
+        case 1: return launch_tokens_as<kSrc, 512, 1>(p, st);
+        case 2: return launch_tokens_as<kSrc, 512, 2>(p, st);
+        case 3:
+        case 4: return launch_tokens_as<kSrc, 512, 4>(p, st);
+        default: return launch_tokens_as<kSrc, 512, 0>(p, st);
+    }
 }
 
 // x_cols: elements of a row that are read (K, or 2K for the SwiGLU).
@@ -68,8 +98,8 @@ int tokens_common(const void *X, int dtype, bool swiglu, int64_t ldx, int64_t M,
     if (rc != W8_OK) return rc;
     const tokens::Params p = {X, ldx, M, K, q, ldq, scales, sums};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (swiglu) return launch_tokens<tokens::kSwiglu>(p, st);
-    return dtype == W8_F32 ? launch_tokens<tokens::kF32>(p, st) : launch_tokens<tokens::kF16>(p, st);
+    if (swiglu) return launch_tokens<tokens::kSwiglu>(d, p, st);
+    return dtype == W8_F32 ? launch_tokens<tokens::kF32>(d, p, st) : launch_tokens<tokens::kF16>(d, p, st);
 }
 
 // ---------------------------------------------------------------- W8A8 linear

@@ -161,3 +161,26 @@ def test_refusals():
     for bad in (X.float(), X[:, :63]):
         with pytest.raises(ValueError):
             m.swiglu_quantize_tokens(bad)
+
+
+def test_swiglu_every_gate_value():
+    # one row for each finite fp16 gate g: its only product sets the row's
+    # scale, which shows h = g / (1 + exp(-g)) u to a unit in the last place.
+    # The steps after CUDA's exp (here through torch) are correctly rounded:
+    # float64 and one rounding give the same.
+    import torch
+    g = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.float16)
+    g = g[torch.isfinite(g)]
+    e = torch.exp(-g.float()).cpu().numpy()
+    gate = g.cpu().numpy().astype(np.float64)
+    with np.errstate(over="ignore", invalid="ignore"):
+        silu = (gate / (np.float32(1) + e).astype(np.float64)).astype(np.float32)
+    for u in (1.0, 127.0, 0.3):
+        H = torch.zeros((g.numel(), 16), dtype=torch.float16, device="cuda")
+        H[:, 3] = g
+        H[:, 11] = u
+        _, s, sums = (to_np(t) for t in w8().swiglu_quantize_tokens(H))
+        h = (silu.astype(np.float64) * np.float64(np.float16(u))).astype(np.float32)
+        want = (np.abs(h).astype(np.float64) / 127).astype(np.float32)
+        assert np.array_equal(s, want)
+        assert np.array_equal(np.abs(sums), np.where(want > 0, 127, 0))
