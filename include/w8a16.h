@@ -337,20 +337,25 @@ int w8_swiglu_quantize_per_token(const uint16_t *H, int64_t ldh, int64_t M, int6
  *   Y         [M, N] fp16; must not overlap any input.
  *   M >= 0 (0 is a no-op); K >= 1 with K % 8 == 0 and K <= 65536 (the sums
  *   stay below 2^31 whatever the codes are); N >= 1 with N % 8 == 0.
- *   workspace of w8a8_workspace_bytes(M, K, N) bytes: the workspace of
- *             w8a16_linear, same size, same rules; one buffer serves both.
+ *   No workspace: the call keeps nothing in memory of its own, so calls on
+ *   different streams and captured graphs may overlap.
+ * Kernel choice (internal): up to 128 tokens, and beyond where the product is
+ *   small, output tiles of 128 channels on single SMs, one cluster of 2 to 8
+ *   thread blocks for each (split over K, the sums gathered in distributed
+ *   shared memory) where the tiles are few; else pairs of SMs with tiles of
+ *   256 channels x 128 or 256 tokens.  All run the 8-bit integer tcgen05
+ *   product on the packed weight as it stands.
  * Results: the integer sum is exact and independent of how the work is split;
  *   fp32 rounds it, the product with s_m and the fused product with s_n plus
  *   bias, and fp16 the result: |Y - Y_exact| <= 2^-11 |Y_exact| + 2^-22 (|Y_exact -
  *   bias| + |Y_exact|) in fp16's normal range.  Bit-identical on every call.
  * Stream ordering as w8a16_linear.
- * Errors: W8_ERR_NULL, W8_ERR_SHAPE, W8_ERR_ALIGN, W8_ERR_WORKSPACE,
- *         W8_ERR_ALIAS, W8_ERR_DEVICE, W8_ERR_CUDA.
+ * Errors: W8_ERR_NULL, W8_ERR_SHAPE, W8_ERR_ALIGN, W8_ERR_ALIAS,
+ *         W8_ERR_DEVICE, W8_ERR_CUDA.
  */
-size_t w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N);
 int w8a8_linear(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums, const uint8_t *packed,
                 const uint16_t *scales, const int8_t *zeros, const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K,
-                int64_t N, void *workspace, size_t workspace_bytes, void *stream);
+                int64_t N, void *stream);
 
 /*
  * w8a8_linear_grouped -- w8a8_linear with one weight per group of rows (the
@@ -371,7 +376,7 @@ int w8a8_linear(const int8_t *q, int64_t ldq, const float *x_scales, const int32
 int w8a8_linear_grouped(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums,
                         const int32_t *offsets, int64_t groups, const uint8_t *packed, const uint16_t *scales,
                         const int8_t *zeros, const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K, int64_t N,
-                        void *workspace, size_t workspace_bytes, void *stream);
+                        void *stream);
 
 /*
  * w8a16_linear_decode_static -- the decode path of w8a16_linear (M <= 16)

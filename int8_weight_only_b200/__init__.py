@@ -90,10 +90,8 @@ def load_library():
         lib.w8a16_linear_decode_static.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp]
         lib.w8_quantize_per_token.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp]
         lib.w8_swiglu_quantize_per_token.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp, vp]
-        lib.w8a8_workspace_bytes.argtypes = [i64, i64, i64]
-        lib.w8a8_workspace_bytes.restype = sz
-        lib.w8a8_linear.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
-        lib.w8a8_linear_grouped.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
+        lib.w8a8_linear.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp]
+        lib.w8a8_linear_grouped.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, vp]
         lib.w8_error_string.argtypes = [i32]
         lib.w8_error_string.restype = ctypes.c_char_p
         lib.w8_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
@@ -510,33 +508,6 @@ def _call(fn, what, device, stream, *args):
         raise W8Error(rc, what)
 
 
-_ws_need = {}
-
-
-def _w8a8_workspace(device, stream, K, N, workspace):
-    """The scratch of a linear_w8a8 call.  Without one from the caller: the
-    stream's default buffer, or, while a graph is captured, memory of that
-    graph (two graphs replayed at once must not share it) whose counters
-    the graph itself clears."""
-    torch = _torch()
-    if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {device}")
-        return workspace
-    need = _ws_need.get((device.index, N))
-    if need is None:
-        with torch.cuda.device(device):
-            need = _ws_need[(device.index, N)] = int(load_library().w8a8_workspace_bytes(1, K, N))
-    if not torch.cuda.is_current_stream_capturing():
-        buf = _ws_cache.get((device.index, stream))
-        return buf if buf is not None and buf.numel() >= need else _workspace(device, need)
-    sms = torch.cuda.get_device_properties(device).multi_processor_count
-    counters = max((N + 127) // 128, 2 * sms) * 4
-    workspace = torch.empty((need,), dtype=torch.uint8, device=device)
-    workspace[need - (counters + 255) // 256 * 256:].zero_()
-    return workspace
-
-
 def _token_outputs(M, K, device, q, scales, sums):
     torch = _torch()
     if q is None:
@@ -626,23 +597,20 @@ def _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, lead):
     return ldq, M, K, N, out
 
 
-def linear_w8a8(q, x_scales, x_sums, packed, scales, bias=None, zeros=None, out=None, workspace=None):
+def linear_w8a8(q, x_scales, x_sums, packed, scales, bias=None, zeros=None, out=None):
     """Y [M, N] fp16 = x_scales scales (q . (w - zeros)) (+ bias) for the
     output of quantize_tokens (or of swiglu_quantize_tokens) and a packed
     weight; zeros for codes from quantize_asym."""
     lib = load_library()
     ldq, M, K, N, out = _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, ())
     dev = q.device
-    stream = _raw_stream(dev)
-    ws = _w8a8_workspace(dev, stream, K, N, workspace)
-    _call(lib.w8a8_linear, "w8a8_linear", dev, stream, q.data_ptr(), ldq, x_scales.data_ptr(), x_sums.data_ptr(),
+    _call(lib.w8a8_linear, "w8a8_linear", dev, _raw_stream(dev), q.data_ptr(), ldq, x_scales.data_ptr(), x_sums.data_ptr(),
           packed.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
-          None if bias is None else bias.data_ptr(), out.data_ptr(), M, K, N, ws.data_ptr(), ws.numel() * ws.element_size())
+          None if bias is None else bias.data_ptr(), out.data_ptr(), M, K, N)
     return out
 
 
-def linear_w8a8_grouped(q, x_scales, x_sums, offsets, packed, scales, bias=None, zeros=None, out=None,
-                        workspace=None):
+def linear_w8a8_grouped(q, x_scales, x_sums, offsets, packed, scales, bias=None, zeros=None, out=None):
     """linear_w8a8 with one weight per group of rows: rows [offsets[e],
     offsets[e + 1]) of q times weight e.  offsets: int32 [E + 1] on the device
     (never read by the host); packed: uint8 [E, prepacked_bytes(K, N)];
@@ -656,12 +624,10 @@ def linear_w8a8_grouped(q, x_scales, x_sums, offsets, packed, scales, bias=None,
     ldq, M, K, N, out = _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, (E,))
     dev = q.device
     _need(offsets, "offsets", torch.int32, (E + 1,), dev)
-    stream = _raw_stream(dev)
-    ws = _w8a8_workspace(dev, stream, K, N, workspace)
-    _call(lib.w8a8_linear_grouped, "w8a8_linear_grouped", dev, stream, q.data_ptr(), ldq, x_scales.data_ptr(),
+    _call(lib.w8a8_linear_grouped, "w8a8_linear_grouped", dev, _raw_stream(dev), q.data_ptr(), ldq, x_scales.data_ptr(),
           x_sums.data_ptr(), offsets.data_ptr(), E, packed.data_ptr(), scales.data_ptr(),
           None if zeros is None else zeros.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(),
-          M, K, N, ws.data_ptr(), ws.numel() * ws.element_size())
+          M, K, N)
     return out
 
 

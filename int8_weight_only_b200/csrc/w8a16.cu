@@ -32,7 +32,6 @@ struct DeviceInfo {
     int status = W8_OK;   // W8_ERR_DEVICE if not sm_100
     int sms = 0;
     int pairs = 0;   // resident prefill CTA pairs (0 = not yet queried)
-    int i8pairs[2] = {};   // the same of the W8A8 pair kernel: one weight, grouped
     // resident quantize clusters per cluster size (0 = not yet queried)
     int qclusters_f32[quant::kMaxCluster + 1] = {};
     int qclusters_f16[quant::kMaxCluster + 1] = {};

@@ -179,21 +179,18 @@ int launch_w8a8_cluster(int c, int64_t units, const int8_t *q, int64_t ldq, int6
     return launch_status();
 }
 
-template <int TN, bool kGrouped>
+template <int TN>
 int launch_w8a8_as(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
-    if constexpr (!kGrouped) {
-        const int64_t units = cdiv(p.rows, TN) * p.NB;
-        const int c = w8a8_cluster_size<TN>(d, units, p.KB);
-        if (c > 0) return launch_w8a8_cluster<TN>(c, units, q, ldq, K, p, st);
-    }
+    const int64_t units = cdiv(p.rows, TN) * p.NB;
+    const int c = w8a8_cluster_size<TN>(d, units, p.KB);
+    if (c > 0) return launch_w8a8_cluster<TN>(c, units, q, ldq, K, p, st);
     CUtensorMap map;
     const int rc = make_map_codes(&map, q, ldq, p.rows, K, TN);
     if (rc != W8_OK) return rc;
     cudaLaunchConfig_t cfg = {};
-    // one block per multiprocessor, as far as the workspace has room for
-    // the two shared output tiles of each
-    const int64_t slots = (int64_t)(partial_area_bytes(d->sms) / (2 * (size_t)TN * w8a8::kBN * sizeof(int32_t)));
-    cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(d->sms, slots)), 1, 1);
+    // blocks with equally many output tiles, as far as they divide
+    const int64_t each = cdiv(units, d->sms);
+    cfg.gridDim = dim3((unsigned)cdiv(units, each), 1, 1);
     cfg.blockDim = dim3(w8a8::Cfg<TN>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = w8a8::Cfg<TN>::kSmemBytes;
     cfg.stream = st;
@@ -202,27 +199,29 @@ int launch_w8a8_as(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, w8a8::w8a8_kernel<TN, kGrouped>, map, p) != cudaSuccess) return cuda_fail();
+    if (cudaLaunchKernelEx(&cfg, w8a8::w8a8_kernel<TN>, map, p) != cudaSuccess) return cuda_fail();
     return launch_status();
 }
 
 // Many tokens: pairs of SMs (w8a8_pair.cuh).
-template <bool kGrouped>
+template <int BT, bool kGrouped>
 int launch_w8a8_pair(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
     namespace wp = w8a8::pair;
-    CUtensorMap map_x, map_w;
-    int rc = make_map_codes(&map_x, q, ldq, p.rows, K, wp::kBT / 2);
+    wp::Maps maps;
+    CUtensorMap map_w;
+    int rc = W8_OK;
+    for (int i = 0; i < wp::kXMaps && rc == W8_OK; ++i) rc = make_map_codes(&maps.x[i], q, ldq, p.rows, K, BT / 2 >> i);
     if (rc != W8_OK) return rc;
     // coordinates of rows of 128 packed bytes and tile numbers are 32-bit
     const int64_t wrows = (int64_t)p.groups * p.NB * p.KB * (w8a8::kTile / 128);
-    const int64_t most_tiles = (cdiv(p.rows, wp::kBT) + p.groups) * cdiv(p.NB, 2);
+    const int64_t most_tiles = (cdiv(p.rows, BT) + p.groups) * cdiv(p.NB, 2);
     if (wrows > (int64_t)INT32_MAX - 128 || most_tiles > INT32_MAX / 2) return W8_ERR_SHAPE;
     rc = make_map_2d(&map_w, p.packed, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128, (uint64_t)wrows, 128, 128,
                      CU_TENSOR_MAP_SWIZZLE_NONE);
     if (rc != W8_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(wp::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = wp::kSmemBytes;
+    cfg.dynamicSmemBytes = wp::Cfg<BT>::kSmemBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -233,38 +232,60 @@ int launch_w8a8_pair(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, con
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;   // the occupancy query takes the cluster shape only
+    const void *fn = (const void *)wp::w8a8_pair_kernel<BT, kGrouped>;
     int pairs = 0;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        int &cached = d->i8pairs[kGrouped ? 1 : 0];
+        int &cached = d->dclusters[{fn, 2}];
         if (cached == 0) {
-            cfg.gridDim = dim3((unsigned)d->sms, 1, 1);
+            cfg.gridDim = dim3((unsigned)(d->sms / 2 * 2), 1, 1);
             int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, wp::w8a8_pair_kernel<kGrouped>, &cfg) != cudaSuccess || n < 1) {
+            if (cudaOccupancyMaxActiveClusters(&n, wp::w8a8_pair_kernel<BT, kGrouped>, &cfg) != cudaSuccess || n < 1) {
                 cudaGetLastError();
                 n = d->sms / 2;
             }
-            cached = std::max(1, std::min(n, d->sms / 2));   // the workspace has parts for sms / 2 pairs
+            cached = std::max(1, n);
         }
         pairs = cached;
     }
+    if (!kGrouped) pairs = (int)std::min<int64_t>(pairs, most_tiles);
     cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, wp::w8a8_pair_kernel<kGrouped>, map_w, map_x, p) != cudaSuccess) return cuda_fail();
+    if (cudaLaunchKernelEx(&cfg, wp::w8a8_pair_kernel<BT, kGrouped>, map_w, maps, p) != cudaSuccess) return cuda_fail();
     return launch_status();
 }
 
-// More tokens (a group, on average) than this go to the pairs.
-constexpr int64_t kPairFrom = 128;
+// The kernel of a product of one weight.  Up to 128 tokens: one token tile,
+// split over K (w8a8.cuh, w8a8_cluster.cuh).  Above, whichever of three ways
+// is shortest by a line through measured times, in microseconds: a tile's K
+// steps of 128 features take 0.32 (256 tokens a tile, pairs of SMs) or 0.24
+// (128 tokens), a weight tile of 64 features 0.17 (128 tokens, one SM), and a
+// call 4.9, 4.2 and 3.9 besides.  Measured / by the line: 512 x 4096 x 4096
+// 14.1 / 15.1, 12.0 / 11.9, 18.8 / 14.8; 512 x 8016 x 1312 21.8 / 25.1, 18.3 /
+// 19.3, 15.0 / 14.6; 2048 x 8016 x 1312 24.0 / 25.1, 33.2 / 34.4, 31.7 / 46.7.
+int launch_w8a8(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
+    const int64_t M = p.rows;
+    if (M <= 16) return launch_w8a8_as<16>(d, q, ldq, K, p, st);
+    if (M <= 32) return launch_w8a8_as<32>(d, q, ldq, K, p, st);
+    if (M <= 64) return launch_w8a8_as<64>(d, q, ldq, K, p, st);
+    if (M <= 128) return launch_w8a8_as<128>(d, q, ldq, K, p, st);
+    const int64_t pairs = std::max(1, d->sms / 2), steps = cdiv(p.KB, 2), units = cdiv(M, 128) * p.NB;
+    const double t256 = 4.9 + 0.32 * (double)(cdiv(cdiv(M, 256) * cdiv(p.NB, 2), pairs) * steps);
+    const double t128 = 4.2 + 0.24 * (double)(cdiv(cdiv(M, 128) * cdiv(p.NB, 2), pairs) * steps);
+    const int c = w8a8_cluster_size<128>(d, units, p.KB);
+    const double one = 3.9 + 0.17 * (double)(c > 0 ? cdiv(p.KB, c) : cdiv(units, d->sms) * p.KB);
+    if (one < t128 && one < t256) return launch_w8a8_as<128>(d, q, ldq, K, p, st);
+    if (t128 < t256) return launch_w8a8_pair<128, false>(d, q, ldq, K, p, st);
+    return launch_w8a8_pair<256, false>(d, q, ldq, K, p, st);
+}
 
-template <bool kGrouped>
-int launch_w8a8(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, int64_t tokens,
-                cudaStream_t st) {
-    if (tokens > kPairFrom) return launch_w8a8_pair<kGrouped>(d, q, ldq, K, p, st);
-    if (tokens <= 16) return launch_w8a8_as<16, kGrouped>(d, q, ldq, K, p, st);
-    if (tokens <= 32) return launch_w8a8_as<32, kGrouped>(d, q, ldq, K, p, st);
-    if (tokens <= 64) return launch_w8a8_as<64, kGrouped>(d, q, ldq, K, p, st);
-    return launch_w8a8_as<128, kGrouped>(d, q, ldq, K, p, st);
+// The kernel of a grouped product, by the mean group (the groups themselves
+// are known on the device only): tiles of 256 tokens from 96 tokens on.  8
+// groups of 4096 x 4096, microseconds with tiles of 128 / 256: 16 tokens each
+// 24.6 / 25.9, 64 25.9 / 27.6, 128 31.2 / 30.2, 256 46.0 / 40.0.
+int launch_w8a8_grouped(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
+    if (p.rows > 96 * (int64_t)p.groups) return launch_w8a8_pair<256, true>(d, q, ldq, K, p, st);
+    return launch_w8a8_pair<128, true>(d, q, ldq, K, p, st);
 }
 
 cudaError_t w8a8_attributes() {
@@ -279,17 +300,22 @@ cudaError_t w8a8_attributes() {
     W8_I8_CLUSTER_SMEM(128)
 #undef W8_I8_CLUSTER_SMEM
 #define W8_I8_SMEM(TN)                                                                                        \
-    for (const void *f : {(const void *)w8a8::w8a8_kernel<TN, false>, (const void *)w8a8::w8a8_kernel<TN, true>}) \
-        if (e == cudaSuccess)                                                                                 \
-            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, w8a8::Cfg<TN>::kSmemBytes);
+    if (e == cudaSuccess)                                                                                     \
+        e = cudaFuncSetAttribute((const void *)w8a8::w8a8_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
+                                 w8a8::Cfg<TN>::kSmemBytes);
     W8_I8_SMEM(16)
     W8_I8_SMEM(32)
     W8_I8_SMEM(64)
     W8_I8_SMEM(128)
 #undef W8_I8_SMEM
-    for (const void *f : {(const void *)w8a8::pair::w8a8_pair_kernel<false>, (const void *)w8a8::pair::w8a8_pair_kernel<true>})
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, w8a8::pair::kSmemBytes);
+#define W8_I8_PAIR_SMEM(BT)                                                                                   \
+    for (const void *f : {(const void *)w8a8::pair::w8a8_pair_kernel<BT, false>,                             \
+                          (const void *)w8a8::pair::w8a8_pair_kernel<BT, true>})                              \
+        if (e == cudaSuccess)                                                                                 \
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, w8a8::pair::Cfg<BT>::kSmemBytes);
+    W8_I8_PAIR_SMEM(128)
+    W8_I8_PAIR_SMEM(256)
+#undef W8_I8_PAIR_SMEM
     return e;
 }
 
@@ -297,18 +323,16 @@ cudaError_t w8a8_attributes() {
 // per group.
 int w8a8_common(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums, const int32_t *offsets,
                 bool grouped, int64_t groups, const uint8_t *packed, const uint16_t *scales, const int8_t *zeros,
-                const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K, int64_t N, void *workspace,
-                size_t workspace_bytes, void *stream) {
+                const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K, int64_t N, void *stream) {
     if (M < 0 || K < 1 || N < 1 || K % 8 != 0 || N % 8 != 0 || K > kMaxSumK || M > (int64_t)INT32_MAX - 512 ||
         N > (1LL << 30) || ldq < K || ldq % 16 != 0 || ldq >= (1LL << 40))
         return W8_ERR_SHAPE;
-    if (grouped && (groups < 1 || groups > w8a8::kMaxGroups || M > kMaxGroupedRows)) return W8_ERR_SHAPE;
+    if (grouped && (groups < 1 || groups > w8a8::pair::kMaxGroups || M > kMaxGroupedRows)) return W8_ERR_SHAPE;
     if (!packed || !scales || (grouped && !offsets)) return W8_ERR_NULL;
     if (M == 0) return W8_OK;   // no rows: nothing to read or write
     if (!q || !x_scales || !x_sums || !Y) return W8_ERR_NULL;
     if (!aligned16(q) || !aligned16(x_scales) || !aligned16(x_sums) || !aligned16(packed) || !aligned16(scales) ||
-        !aligned16(Y) || (bias && !aligned16(bias)) || (zeros && !aligned16(zeros)) || (offsets && !aligned16(offsets)) ||
-        (workspace && !aligned16(workspace)))
+        !aligned16(Y) || (bias && !aligned16(bias)) || (zeros && !aligned16(zeros)) || (offsets && !aligned16(offsets)))
         return W8_ERR_ALIGN;
     const size_t yb = (size_t)M * N * 2, qb = span(M, ldq, K, 1), wb = (size_t)groups * w8_prepacked_bytes(K, N),
                  sb = (size_t)groups * N * 2;
@@ -319,9 +343,6 @@ int w8a8_common(const int8_t *q, int64_t ldq, const float *x_scales, const int32
     DeviceInfo *d = nullptr;
     int rc = device_info(&d);
     if (rc != W8_OK) return rc;
-    const size_t need = workspace_total(d->sms, N);
-    if (!workspace || workspace_bytes < need) return W8_ERR_WORKSPACE;
-    if (overlap(workspace, need, Y, yb) || overlap(workspace, need, q, qb)) return W8_ERR_ALIAS;
     w8a8::Params p = {};
     p.packed = packed;
     p.scales = scales;
@@ -331,16 +352,13 @@ int w8a8_common(const int8_t *q, int64_t ldq, const float *x_scales, const int32
     p.x_sums = x_sums;
     p.offsets = offsets;
     p.Y = Y;
-    p.partials = static_cast<int32_t *>(workspace);
-    p.counters = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + partial_area_bytes(d->sms));
     p.rows = M;
     p.N = N;
     p.groups = (int)groups;
     p.NB = (int)cdiv(N, 128);
     p.KB = (int)cdiv(K, 64);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (grouped) return launch_w8a8<true>(d, q, ldq, K, p, cdiv(M, groups), st);
-    return launch_w8a8<false>(d, q, ldq, K, p, M, st);
+    return grouped ? launch_w8a8_grouped(d, q, ldq, K, p, st) : launch_w8a8(d, q, ldq, K, p, st);
 }
 
 }  // namespace
@@ -357,21 +375,18 @@ int w8_swiglu_quantize_per_token(const uint16_t *H, int64_t ldh, int64_t M, int6
     return tokens_common(H, W8_F16, true, ldh, M, K, q, ldq, scales, sums, stream);
 }
 
-size_t w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N) { return w8a16_workspace_bytes(M, K, N); }
-
 int w8a8_linear(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums, const uint8_t *packed,
                 const uint16_t *scales, const int8_t *zeros, const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K,
-                int64_t N, void *workspace, size_t workspace_bytes, void *stream) {
-    return w8a8_common(q, ldq, x_scales, x_sums, nullptr, false, 1, packed, scales, zeros, bias, Y, M, K, N, workspace,
-                       workspace_bytes, stream);
+                int64_t N, void *stream) {
+    return w8a8_common(q, ldq, x_scales, x_sums, nullptr, false, 1, packed, scales, zeros, bias, Y, M, K, N, stream);
 }
 
 int w8a8_linear_grouped(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums,
                         const int32_t *offsets, int64_t groups, const uint8_t *packed, const uint16_t *scales,
                         const int8_t *zeros, const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K, int64_t N,
-                        void *workspace, size_t workspace_bytes, void *stream) {
+                        void *stream) {
     return w8a8_common(q, ldq, x_scales, x_sums, offsets, true, groups, packed, scales, zeros, bias, Y, M, K, N,
-                       workspace, workspace_bytes, stream);
+                       stream);
 }
 
 }  // extern "C"

@@ -1,18 +1,23 @@
 // W8A8 linear for many tokens, on pairs of SMs (tcgen05 cta_group::2): the
-// product of w8a8.cuh with output tiles of 256 channels x up to 256 tokens.
-// Each block of a cluster of two holds its own 128 channels of the weight and
-// half of the tile's tokens in shared memory, so a 128-wide K step brings 32
-// KB into each SM for 512 cycles of integer products; the 32-bit sums of two
-// tiles fit in tensor memory, and a tile is scaled and stored while the next
-// one runs.
+// product of w8a8.cuh with output tiles of 256 channels x BT tokens (256, or
+// 128 where tiles of 256 would not fill the GPU).  Each block of a cluster of
+// two holds its own 128 channels of the weight and half of the tile's tokens
+// in shared memory, so a 128-wide K step of a 256 x 256 tile brings 32 KB into
+// each SM for 512 cycles of integer products; the 32-bit sums of two tiles fit
+// in tensor memory, and a tile is scaled and stored while the next one runs.
 //
-// Schedule: whole tiles round robin over the pairs; where that leaves pairs
-// idle in the last wave for long, the K steps of the last tiles are split
-// evenly instead (integer parts, added by the last block to arrive).
+// Schedule: whole tiles, round robin over the pairs.  Splitting the K steps of
+// the last tiles evenly over the pairs, the parts added through the workspace,
+// was slower wherever it was tried: a block's part of a tile is 128 KB, which
+// one SM takes more than a microsecond to write or read (256 x 4096 x 27392,
+// two waves of tiles: 29.3 us whole, 34.5 split; 512 x 4096 x 4096, half a
+// wave: 14.1 whole, 24.9 split).
 //
 // Roles in each block: warp 0 producer, warp 1 products (first block), warp 2
 // tensor memory, warps 4-11 scale and store.
 #pragma once
+
+#include <type_traits>
 
 #include "w8a8.cuh"
 
@@ -20,111 +25,107 @@ namespace w8 {
 namespace w8a8 {
 namespace pair {
 
-constexpr int kBT = 256;                     // tokens of a tile
 constexpr int kStepTiles = 2;                // weight tiles per stage (128 features)
 constexpr int kWBytes = kStepTiles * kTile;
-constexpr int kXBytes = (kBT / 2) * 128;     // 128 tokens x 128 features
-constexpr int kStageBytes = kWBytes + kXBytes;
-constexpr int kStages = 5;
 constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kParts = kEpiWarps / 4;        // a warp reads 32 of the 128 channels, of one part of the tokens
-constexpr int kPartTokens = kBT / kParts;
 // Outputs on their way out, per warp two buffers of kChunk tokens x its 32
 // channels fp16; the 16-byte piece c of token t lies at piece c ^ (t / 2 & 3).
 constexpr int kChunk = 32;
 constexpr int kOutBuf = kChunk * 32 * 2;
 constexpr int kOutBytes = kEpiWarps * 2 * kOutBuf;
-constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024;
-constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr uint32_t kTmemCols = 2 * kBT;
-constexpr int kPartSums = kBT * kBN;             // 32-bit sums of one block's share of a tile
 constexpr uint16_t kBoth = 0x3;
-// K steps per pair that splitting the last tiles has to save
-constexpr int kSplitMin = 12;
+// The tokens' tensor map comes with three box heights, BT / 2 rows and a half
+// and a quarter of that: a short tile takes the lowest that holds its half.
+constexpr int kXMaps = 3;
+
+template <int BT>
+struct Cfg {
+    static constexpr int kXBytes = BT / 2 * 128;             // half of the tokens x 128 features
+    static constexpr int kStageBytes = kWBytes + kXBytes;
+    static constexpr int kStages = BT == 256 ? 5 : 7;
+    static constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024;
+    static constexpr uint32_t kTmemCols = 2 * BT;
+    static constexpr int kPartTokens = BT / kParts;
+};
+
+struct Maps {
+    CUtensorMap x[kXMaps];
+};
+
+constexpr int kMaxGroups = 1024;
+// The groups' rows and token tiles, in shared memory.
+struct Groups {
+    int first[kMaxGroups + 1];    // first row, within [0, rows]
+    int tiles[kMaxGroups + 1];    // token tiles of all groups before
+};
+struct OneGroup {};
+
+// All kThreads_ threads of the block; a block barrier has to follow.  The
+// first rows are clamped to [0, rows], so no offset can lead out of bounds.
+template <int TN, int kThreads_>
+__device__ __forceinline__ void load_groups(const Params &p, Groups &g) {
+    for (int e = threadIdx.x; e <= p.groups; e += kThreads_) g.first[e] = (int)max64(0, min64(p.rows, p.offsets[e]));
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int before = 0;
+        if (lane == 0) g.tiles[0] = 0;
+        for (int e0 = 0; e0 < p.groups; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < p.groups) n = (max(0, g.first[e + 1] - g.first[e]) + TN - 1) / TN;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, n, d);
+                if (lane >= d) n += o;
+            }
+            if (e < p.groups) g.tiles[e + 1] = before + n;
+            before += __shfl_sync(0xffffffffu, n, 31);
+        }
+    }
+}
 
 struct Seg {
     int group, nbp, tt;
-    int ks0, ks1;
-    int tile;
-    int slot;       // -1: the whole tile; else the slot of its part
 };
 
-// Tiles [0, dp) go round robin, the K steps of the others evenly over `pairs`.
-struct Plan {
-    int tiles, dp, pairs;
-    int64_t steps;     // K steps of the split tiles
-    __device__ Plan(int64_t n, int P, int KS) {
-        tiles = (int)n;
-        dp = tiles;
-        pairs = P;
-        steps = 0;
-        const int64_t whole = (n + P - 1) / P * KS;
-        const int64_t sk = n % P == 0 ? 0 : (n > P ? P + n % P : n);
-        const int64_t split = (n - sk) / P * KS + (sk * KS + P - 1) / P;
-        if (whole - split >= kSplitMin) {
-            dp = (int)(n - sk);
-            steps = sk * KS;
-            pairs = (int)min64(P, steps);
-        }
-    }
-    __device__ int64_t begin(int64_t q) const { return q * steps / pairs; }
-    __device__ int owner(int64_t it) const { return (int)(((it + 1) * pairs - 1) / steps); }
-    __device__ int slot(int q, int tile, int KS) const { return dp + (int)(begin(q) / KS) == tile ? 0 : 1; }
-};
-
-template <bool kGrouped>
+template <int BT, bool kGrouped>
 struct Sched {
     const Groups *g;
-    Plan plan;
-    int NBP, KS, TT, tile, P, group;
-    int64_t it, end;
-    int q;
-    __device__ Sched(const Params &p, const Groups *groups, const Plan &pl, int pair, int P_)
-        : g(groups), plan(pl), NBP((p.NB + 1) / 2), KS((p.KB + 1) / 2), TT((int)((p.rows + kBT - 1) / kBT)), tile(pair),
-          P(P_), group(0), q(pair) {
-        it = end = 0;
-        if (plan.steps > 0 && pair < plan.pairs) {
-            it = plan.begin(pair);
-            end = plan.begin(pair + 1);
-        }
-    }
+    int NBP, TT, group, step;
+    int64_t tile, tiles;
+    __device__ Sched(const Params &p, const Groups *groups, int64_t n_tiles, int pair, int pairs)
+        : g(groups), NBP((p.NB + 1) / 2), TT((int)((p.rows + BT - 1) / BT)), group(0), step(pairs), tile(pair),
+          tiles(n_tiles) {}
     __device__ bool next(Seg &s) {
-        if (tile < plan.dp) {
-            s.tile = tile;
-            s.ks0 = 0;
-            s.ks1 = KS;
-            s.slot = -1;
-            tile += P;
-        } else if (it < end) {
-            const int t = (int)(it / KS);
-            s.tile = plan.dp + t;
-            s.ks0 = (int)(it - (int64_t)t * KS);
-            s.ks1 = (int)min64(KS, s.ks0 + (end - it));
-            s.slot = s.ks0 == 0 && s.ks1 == KS ? -1 : plan.slot(q, s.tile, KS);
-            it += s.ks1 - s.ks0;
-        } else {
-            return false;
-        }
-        int local = s.tile, tt_n = TT;
+        if (tile >= tiles) return false;
+        int64_t local = tile;
+        int tt_n = TT;
         if constexpr (kGrouped) {
-            while ((int64_t)s.tile >= (int64_t)NBP * g->tiles[group + 1]) ++group;
-            local -= NBP * g->tiles[group];
+            while (tile >= (int64_t)NBP * g->tiles[group + 1]) ++group;
+            local -= (int64_t)NBP * g->tiles[group];
             tt_n = g->tiles[group + 1] - g->tiles[group];
         }
         s.group = group;
-        s.nbp = local / tt_n;
-        s.tt = local - s.nbp * tt_n;
+        // the host keeps the tiles of a call below 2^31
+        s.nbp = (int)local / tt_n;
+        s.tt = (int)local - s.nbp * tt_n;
+        tile += step;
         return true;
     }
 };
 
 // grid = 2 x pairs blocks in clusters of two.  tmap_w: the packed weights as
-// rows of 128 bytes, box 128 x 128 (two tiles), no swizzle; tmap_x: codes
-// [rows, K], box 128 features x 128 rows, 128-byte swizzle.
-template <bool kGrouped>
+// rows of 128 bytes, box 128 x 128 (two tiles), no swizzle; maps: codes
+// [rows, K], boxes of 128 features, 128-byte swizzle.
+template <int BT, bool kGrouped>
 __global__ void __launch_bounds__(kThreads, 1)
-w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ Maps maps,
                  const __grid_constant__ Params p) {
+    using C = Cfg<BT>;
+    constexpr int kStages = C::kStages, kStageBytes = C::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -132,9 +133,8 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ uint64_t d_full[2], d_empty[2], drain;
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int last_sh;
-    __shared__ __align__(16) int sum_sh[2][kBT];
-    __shared__ __align__(16) float xs_sh[2][kBT];
+    __shared__ __align__(16) int sum_sh[2][BT];
+    __shared__ __align__(16) float xs_sh[2][BT];
     using GroupsSh = typename std::conditional<kGrouped, Groups, OneGroup>::type;
     __shared__ GroupsSh groups_sh;
 
@@ -156,38 +156,45 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
         mbar_init(&drain, 1);
         fence_barrier_init();
         prefetch_tensormap(&tmap_w);
-        prefetch_tensormap(&tmap_x);
+        prefetch_tensormap(&maps.x[0]);
     }
     if (warp == 2) {
-        tmem_alloc_pair(&tmem_base_sh, kTmemCols);
+        tmem_alloc_pair(&tmem_base_sh, C::kTmemCols);
         tmem_relinquish_pair();
     }
+    pdl_launch_dependents();
     const Groups *groups = nullptr;
+    if constexpr (kGrouped) groups = reinterpret_cast<const Groups *>(&groups_sh);
+    auto count = [&]() -> int64_t {
+        if constexpr (kGrouped)
+            return (int64_t)groups->tiles[p.groups] * ((p.NB + 1) / 2);
+        else
+            return (p.rows + BT - 1) / BT * ((p.NB + 1) / 2);
+    };
+    // a block's weights of an output tile (the last tile of an odd number of
+    // channel blocks has one block twice)
+    auto block_of = [&](const Seg &s) -> int64_t {
+        return (int64_t)s.group * p.NB + min(2 * s.nbp + (int)rank, p.NB - 1);
+    };
+    // (Bringing the first weights into L2 ahead of the previous kernel's end,
+    // as the kernels for few tokens do, takes a microsecond more here.)
     if constexpr (kGrouped) {
         pdl_wait();
-        load_groups<kBT, kThreads>(p, *reinterpret_cast<Groups *>(&groups_sh));
-        groups = reinterpret_cast<const Groups *>(&groups_sh);
+        load_groups<BT, kThreads>(p, *reinterpret_cast<Groups *>(&groups_sh));
     }
     tc_fence_before();
     cluster_sync_all();
-    pdl_launch_dependents();
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
-    int64_t n_tiles;
-    if constexpr (kGrouped) {
-        n_tiles = (int64_t)groups->tiles[p.groups] * ((p.NB + 1) / 2);
-    } else {
-        n_tiles = (p.rows + kBT - 1) / kBT * ((p.NB + 1) / 2);
-    }
-    const Plan plan(n_tiles, P, KS);
+    const int64_t n_tiles = count();
     auto rows_of = [&](const Seg &s, int64_t &row0) -> int {
         int64_t first = 0, end = p.rows;
         if constexpr (kGrouped) {
             first = groups->first[s.group];
             end = groups->first[s.group + 1];
         }
-        row0 = first + (int64_t)s.tt * kBT;
-        return (int)min64(kBT, end - row0);
+        row0 = first + (int64_t)s.tt * BT;
+        return (int)min64(BT, end - row0);
     };
     // tokens of the product: the tile's, rounded up so that each block holds
     // half of them
@@ -201,20 +208,22 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
             int st = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
-            Sched<kGrouped> sched(p, groups, plan, pair0, P);
+            Sched<BT, kGrouped> sched(p, groups, n_tiles, pair0, P);
             Seg sg;
             while (ok && sched.next(sg)) {
                 int64_t row0;
                 const int n = width(rows_of(sg, row0));
-                const int64_t block = (int64_t)sg.group * p.NB + min(2 * sg.nbp + (int)rank, p.NB - 1);
-                const int wrow = (int)(block * p.KB * (kTile / 128));
+                const int wrow = (int)(block_of(sg) * p.KB * (kTile / 128));
                 const int xrow = (int)row0 + (int)rank * (n / 2);
-                for (int ks = sg.ks0; ks < sg.ks1; ++ks) {
+                const int low = n <= BT / 4 ? 2 : n <= BT / 2 ? 1 : 0;
+                const CUtensorMap *const tmap_x = &maps.x[low];
+                const uint32_t bytes = 2 * (kWBytes + (C::kXBytes >> low));
+                for (int ks = 0; ks < KS; ++ks) {
                     if (!mbar_wait(&empty[st], ph ^ 1u, SITE_I8_EMPTY)) { ok = false; break; }
                     uint8_t *ws = ring + st * kStageBytes;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
                     tma_load_2d_pair(ws, &tmap_w, 0, wrow + ks * (kWBytes / 128), leader(&full[st]));
-                    tma_load_2d_pair(ws + kWBytes, &tmap_x, ks * 128, xrow, leader(&full[st]));
+                    tma_load_2d_pair(ws + kWBytes, tmap_x, ks * 128, xrow, leader(&full[st]));
                     ++issued;
                     if (++st == kStages) { st = 0; ph ^= 1u; }
                 }
@@ -241,16 +250,16 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
             bool ok = true;
             const uint64_t w_desc0 = smem_desc_kmajor_sw64(smem_u32(ring));
             const uint64_t x_desc0 = smem_desc_kmajor_sw128(smem_u32(ring) + kWBytes);
-            Sched<kGrouped> sched(p, groups, plan, pair0, P);
+            Sched<BT, kGrouped> sched(p, groups, n_tiles, pair0, P);
             Seg sg;
             while (ok && sched.next(sg)) {
                 int64_t row0;
                 const uint32_t idesc = idesc_u8_s8_s32(2 * kBN, width(rows_of(sg, row0)));
-                const uint32_t dst = tmem + d * kBT;
+                const uint32_t dst = tmem + d * BT;
                 if (!warp_all(mbar_wait(&d_empty[d], dph ^ 1u, SITE_I8_DEMPTY))) { ok = false; break; }
                 tc_fence_after();
                 uint32_t acc = 0;
-                for (int ks = sg.ks0; ks < sg.ks1; ++ks) {
+                for (int ks = 0; ks < KS; ++ks) {
                     if (!warp_all(mbar_wait(&full[st], ph, SITE_I8_FULL))) { ok = false; break; }
                     tc_fence_after();
                     // descriptors count in units of 16 bytes; the sums stay
@@ -290,7 +299,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
         const int t0 = 2 * (lane & 3);
         int d = 0, buffer = 0;
         uint32_t dph = 0;
-        Sched<kGrouped> sched(p, groups, plan, pair0, P);
+        Sched<BT, kGrouped> sched(p, groups, n_tiles, pair0, P);
         // What the scaling of a tile reads from global memory: its channels'
         // scales, biases and zero points and one token's scale and sum.
         // Loaded a tile ahead, since a tile of short K is over before the
@@ -335,7 +344,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
                 bi2[j] = f32x2(bi, bi);
                 off[j] = 128 + (int)next.z[j];
             }
-            if (c_own < kBT) {
+            if (c_own < BT) {
                 sum_sh[d][c_own] = next.sum;
                 xs_sh[d][c_own] = next.xs;
             }
@@ -386,54 +395,17 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
             };
             if (!named_bar_all(1, 32 * kEpiWarps, mbar_wait(&d_full[d], dph, SITE_I8_DFULL))) break;
             tc_fence_after();
-            const uint32_t src = tmem + ((uint32_t)(32 * q4) << 16) + d * kBT;
-            const int c_end = min(nr, kPartTokens * (part + 1));
-            // parts are kept as each thread holds them: [32 sums of a chunk][thread]
-            auto part_at = [&](int j, int slot, int c0) {
-                return p.partials + ((int64_t)(j * 2 + slot) * 2 + rank) * kPartSums +
-                       (c0 - kPartTokens * part) * (32 * kEpiWarps) + c_own;
-            };
-            for (int c0 = kPartTokens * part; c0 < c_end; c0 += kChunk) {
+            const uint32_t src = tmem + ((uint32_t)(32 * q4) << 16) + d * BT;
+            const int c_end = min(nr, C::kPartTokens * (part + 1));
+            for (int c0 = C::kPartTokens * part; c0 < c_end; c0 += kChunk) {
                 uint32_t v[kChunk];
                 tmem_load_frag_16x32(src + c0, v);
                 tmem_load_frag_16x32(src + (16u << 16) + c0, v + 16);
-                if (sg.slot < 0) {
-                    store(v, c0);
-                } else {
-                    int32_t *const mine = part_at(pair0, sg.slot, c0);
-#pragma unroll
-                    for (int i = 0; i < kChunk; ++i) __stcg(mine + i * (32 * kEpiWarps), (int32_t)v[i]);
-                }
+                store(v, c0);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(leader(&d_empty[d]));
-            if (sg.slot >= 0) {
-                const int64_t it0 = (int64_t)(sg.tile - plan.dp) * KS;
-                const int j0 = plan.owner(it0), j1 = plan.owner(it0 + KS - 1);
-                int *const cnt = p.counters + 2 * j0 + rank;
-                named_bar_sync(1, 32 * kEpiWarps);   // the part is written
-                if (threadIdx.x == 128) {
-                    const int last = atomic_add_acq_rel_gpu(cnt, 1) == j1 - j0;
-                    if (last) *cnt = 0;
-                    last_sh = last;
-                }
-                named_bar_sync(1, 32 * kEpiWarps);
-                if (last_sh) {
-                    for (int c0 = kPartTokens * part; c0 < c_end; c0 += kChunk) {
-                        uint32_t v[kChunk];
-#pragma unroll
-                        for (int i = 0; i < kChunk; ++i) v[i] = 0;
-                        for (int j = j0; j <= j1; ++j) {
-                            const int32_t *const theirs = part_at(j, plan.slot(j, sg.tile, KS), c0);
-#pragma unroll
-                            for (int i = 0; i < kChunk; ++i) v[i] += (uint32_t)__ldcg(theirs + i * (32 * kEpiWarps));
-                        }
-                        store(v, c0);
-                    }
-                }
-                named_bar_sync(1, 32 * kEpiWarps);   // last_sh is read by all
-            }
             if (++d == 2) { d = 0; dph ^= 1u; }
         }
     }
@@ -442,7 +414,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
     cluster_sync_all();
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, kTmemCols);
+        tmem_dealloc_pair(tmem, C::kTmemCols);
     }
 }
 

@@ -48,8 +48,7 @@ def test_swiglu_quantize_per_token_rejects_bad_arguments(w8lib):
 
 def test_linear_rejects_bad_arguments(w8lib):
     f = w8lib.w8a8_linear
-    ws = ctypes.c_void_p(0x200000000)
-    ok = [A, 128, B, C, D, E, None, None, F, 4, 128, 256, ws, 1 << 30, None]
+    ok = [A, 128, B, C, D, E, None, None, F, 4, 128, 256, None]
 
     def call(**kw):
         a = list(ok)
@@ -63,17 +62,16 @@ def test_linear_rejects_bad_arguments(w8lib):
     for i in (0, 2, 3, 4, 5, 8):
         assert call(**{f"_{i}": None}) == -1
         assert call(**{f"_{i}": at(ok[i], 4)}) == -3
-    assert call(_6=at(G, 1)) == -3 and call(_7=at(G, 2)) == -3 and call(_12=at(ws, 8)) == -3
+    assert call(_6=at(G, 1)) == -3 and call(_7=at(G, 2)) == -3
     assert call(_8=at(A, 256)) == -8 and call(_8=at(D, 16)) == -8 and call(_8=E) == -8
     assert call(_6=F) == -8 and call(_7=F) == -8
     assert call(_9=0) == 0
-    assert f(None, 128, None, None, D, E, None, None, None, 0, 128, 256, None, 0, None) == 0
+    assert f(None, 128, None, None, D, E, None, None, None, 0, 128, 256, None) == 0
 
 
 def test_grouped_rejects_bad_arguments(w8lib):
     f = w8lib.w8a8_linear_grouped
-    ws = ctypes.c_void_p(0x200000000)
-    ok = [A, 128, B, C, G, 2, D, E, None, None, F, 4, 128, 256, ws, 1 << 30, None]
+    ok = [A, 128, B, C, G, 2, D, E, None, None, F, 4, 128, 256, None]
 
     def call(**kw):
         a = list(ok)
@@ -94,8 +92,6 @@ def test_well_formed_calls_need_a_device(w8lib):
     import torch
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
-    ws = ctypes.c_void_p(0x200000000)
     assert w8lib.w8_quantize_per_token(A, 1, 64, 4, 64, B, 64, C, D, None) == -6
-    assert w8lib.w8a8_linear(A, 128, B, C, D, E, None, None, F, 4, 128, 256, ws, 1 << 30, None) == -6
-    assert w8lib.w8a8_linear_grouped(A, 128, B, C, G, 2, D, E, None, None, F, 4, 128, 256, ws, 1 << 30, None) == -6
-    assert w8lib.w8a8_workspace_bytes(1, 128, 256) == 0
+    assert w8lib.w8a8_linear(A, 128, B, C, D, E, None, None, F, 4, 128, 256, None) == -6
+    assert w8lib.w8a8_linear_grouped(A, 128, B, C, G, 2, D, E, None, None, F, 4, 128, 256, None) == -6

@@ -12,12 +12,12 @@ def _gpu(a):
     return None if a is None else to_gpu(a)
 
 
-def _run(ops, **kw):
+def _run(ops):
     import torch
     m = w8()
     q, xs, sums, w, scales, zeros, b = ops
     return m.linear_w8a8(pitched(torch, q), _gpu(xs), _gpu(sums), m.prepack(_gpu(w)), _gpu(scales), bias=_gpu(b),
-                         zeros=_gpu(zeros), **kw)
+                         zeros=_gpu(zeros))
 
 
 def _check(ops, got, what=""):
@@ -98,20 +98,19 @@ def test_from_quantized_weights_and_tokens():
     assert np.array_equal(to_np(layer(to_gpu(X))), to_np(m.linear_w8a8(xq, xs, sums, layer.packed, layer.scales)))
 
 
-def test_one_workspace_serves_all_linears():
-    # calls of both activation widths and many shapes through one buffer, each
-    # twice: every call leaves the counters at zero
+def test_calls_in_turn_with_the_w8a16_linear():
+    # the kernels of both activation widths follow one another on one stream,
+    # each launched while the one before ends; every call twice
     import torch
     m = w8()
-    ws = torch.zeros(m.workspace_bytes(1, 4096, 27392), dtype=torch.uint8, device="cuda")
     for M, K, N in [(1, 4096, 384), (20, 13696, 136), (300, 1000, 2048), (4, 4096, 4096), (129, 2048, 384)]:
         ops = operands(M, K, N, M, bias=True)
-        first = to_np(_run(ops, workspace=ws))
+        first = to_np(_run(ops))
         X = torch.randn((M, K), device="cuda").half()
         packed, scales = m.prepack(_gpu(ops[3])), _gpu(ops[4])
-        a = to_np(m.linear(X, packed, scales, workspace=ws))
-        assert np.array_equal(first, to_np(_run(ops, workspace=ws)))
-        assert np.array_equal(a, to_np(m.linear(X, packed, scales, workspace=ws)))
+        a = to_np(m.linear(X, packed, scales))
+        assert np.array_equal(first, to_np(_run(ops)))
+        assert np.array_equal(a, to_np(m.linear(X, packed, scales)))
         _check(ops, torch.from_numpy(first).cuda())
     assert m.device_status() == 0
 
@@ -128,7 +127,7 @@ def test_pitched_codes_slice():
 
 
 # ---------------------------------------------------------------- groups
-def _grouped(counts, K, N, seed, before=0, behind=0, asym=False, bias=False, **kw):
+def _grouped(counts, K, N, seed, before=0, behind=0, asym=False, bias=False):
     """Runs a grouped call and checks every row of Y."""
     import torch
     m = w8()
@@ -138,7 +137,7 @@ def _grouped(counts, K, N, seed, before=0, behind=0, asym=False, bias=False, **k
     packed = torch.stack([m.prepack(_gpu(w[e])) for e in range(E)])
     out = torch.full((M, N), 3.5, dtype=torch.float16, device="cuda")
     got = to_np(m.linear_w8a8_grouped(pitched(torch, q), _gpu(xs), _gpu(sums), _gpu(offsets), packed, _gpu(scales),
-                                      bias=_gpu(b), zeros=_gpu(zeros), out=out, **kw))
+                                      bias=_gpu(b), zeros=_gpu(zeros), out=out))
     for e in range(E):
         r = slice(offsets[e], offsets[e + 1])
         y, prod = linear(q[r], xs[r], w[e], scales[e], None if zeros is None else zeros[e], None if b is None else b[e])
@@ -263,7 +262,7 @@ def test_gated_mlp_of_experts_in_a_graph():
 
 
 def test_two_graphs_replayed_at_once():
-    # each graph has scratch of its own: replays may overlap on the GPU
+    # no call keeps scratch: replays of two graphs may overlap on the GPU
     import torch
     m = w8()
     ops = [operands(9, 4096, 4096, s, bias=True) for s in (1, 2)]
@@ -306,8 +305,6 @@ def test_refusals():
         m.linear_w8a8(**good, out=torch.empty((20, 128), dtype=torch.float16, device="cuda"))
     with pytest.raises(m.W8Error):   # rows not on 16-byte boundaries
         m.linear_w8a8(**{**good, "q": torch.zeros((20, 136), dtype=torch.int8, device="cuda")[:, :128]})
-    with pytest.raises(m.W8Error):
-        m.linear_w8a8(**good, workspace=torch.zeros(1024, dtype=torch.uint8, device="cuda"))
     offsets = torch.tensor([0, 20], dtype=torch.int32, device="cuda")
     grouped = dict(good, packed=packed[None], scales=scales[None], bias=b[None], zeros=zeros[None], offsets=offsets)
     m.linear_w8a8_grouped(**grouped)
