@@ -44,28 +44,26 @@ __device__ __forceinline__ void widen8(const uint4 &v, uint64_t (&f)[4]) {
 // elementwise formula in fp32.
 __device__ __forceinline__ float silu_ieee(float g) { return __fdiv_rn(g, __fadd_rn(1.0f, expf(-g))); }
 
-// The same for two values with |g| <= kSiluFast.  The quotient by Markstein's
-// method (IBM J. Res. Dev. 34(1), 1990): a reciprocal refined once, r, a
-// quotient q = g r and its exact remainder, q + (g - d q) r.  It gives the
-// correctly rounded quotient for every one of the fp16 gates, which
-// tests/test_tokens_gpu.py checks one by one against silu_ieee's values.
+// Minus the same, for two values with |g| <= kSiluFast (the sign spares the
+// negations on the way; the codes undo it).  The quotient by Markstein's method
+// (IBM J. Res. Dev. 34(1), 1990): q = g r with an approximate reciprocal r of
+// d, its exact remainder, q + (g - d q) r.  It gives the correctly rounded
+// quotient for every one of the fp16 gates, which tests/test_tokens_gpu.py
+// checks one by one.
 constexpr float kSiluFast = 80.0f;
 __device__ __forceinline__ float rcp_approx(float d) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
     return r;
 }
-__device__ __forceinline__ uint64_t f32x2_neg(uint64_t a) { return a ^ 0x8000000080000000ull; }
-__device__ __forceinline__ uint64_t silu2(uint64_t g) {
-    const float2 v = f32x2_parts(g);
-    const uint64_t one = f32x2(1.0f, 1.0f);
-    const uint64_t d = f32x2_add(one, f32x2(expf(-v.x), expf(-v.y)));
+__device__ __forceinline__ uint64_t minus_silu2(uint64_t g) {
+    const uint64_t ng = f32x2_mul(g, f32x2(-1.0f, -1.0f));
+    const float2 v = f32x2_parts(ng);
+    const uint64_t d = f32x2_add(f32x2(1.0f, 1.0f), f32x2(expf(v.x), expf(v.y)));
     const float2 dv = f32x2_parts(d);
-    const uint64_t nd = f32x2_neg(d);
-    uint64_t r = f32x2(rcp_approx(dv.x), rcp_approx(dv.y));
-    r = f32x2_fma(r, f32x2_fma(nd, r, one), r);
-    const uint64_t q = f32x2_mul(g, r);
-    return f32x2_fma(f32x2_fma(nd, q, g), r, q);
+    const uint64_t r = f32x2(rcp_approx(dv.x), rcp_approx(dv.y));
+    const uint64_t minus_rem = f32x2_fma(d, f32x2_mul(g, r), ng);
+    return f32x2_fma(minus_rem, r, f32x2_mul(ng, r));
 }
 
 // Bits of the magnitudes of eight values, the largest of each of the four
@@ -78,6 +76,7 @@ __device__ __forceinline__ __half2 max_abs8(const uint4 &g) {
     return m;
 }
 
+// Minus silu(g) u of eight pairs.
 __device__ __forceinline__ void swiglu8(const uint4 &g, const uint4 &u, uint64_t (&f)[4]) {
     uint64_t up[4];
     widen8(g, f);
@@ -85,17 +84,18 @@ __device__ __forceinline__ void swiglu8(const uint4 &g, const uint4 &u, uint64_t
     // (false for NaN: those take the plain formula)
     if (__hble2(max_abs8(g), __float2half2_rn(kSiluFast))) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = f32x2_mul(silu2(f[i]), up[i]);
+        for (int i = 0; i < 4; ++i) f[i] = f32x2_mul(minus_silu2(f[i]), up[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 v = f32x2_parts(f[i]);
-            f[i] = f32x2_mul(f32x2(silu_ieee(v.x), silu_ieee(v.y)), up[i]);
+            f[i] = f32x2_mul(f32x2(-silu_ieee(v.x), -silu_ieee(v.y)), up[i]);
         }
     }
 }
 
-// Eight consecutive values of a row, from element k.
+// Eight consecutive values of a row, from element k (of the SwiGLU with the
+// sign turned).
 template <int kSrc>
 __device__ __forceinline__ void load8(const Params &p, int64_t row, int64_t k, uint64_t (&f)[4]) {
     if constexpr (kSrc == kF32) {
@@ -111,23 +111,26 @@ __device__ __forceinline__ void load8(const Params &p, int64_t row, int64_t k, u
     }
 }
 
-// What the codes of a row need: its scale and 1 / scale.  A scale below
-// fp32's normal range has no usable reciprocal: NaN sends every value to the
-// IEEE quotient.
+// What the codes of a row need: its scale and the reciprocal, with the sign
+// that the values carry.  A scale below fp32's normal range has no usable
+// reciprocal: NaN sends every value to the IEEE quotient.
+template <int kSrc>
 struct RowScale {
+    static constexpr float kSign = kSrc == kSwiglu ? -1.0f : 1.0f;
     float s, inv;
     __device__ explicit RowScale(float amax) {
         s = __fdiv_rn(amax, 127.0f);
-        inv = s >= 1.17549435e-38f ? __fdiv_rn(1.0f, s) : __int_as_float(0x7fffffff);
+        inv = s >= 1.17549435e-38f ? __fdiv_rn(kSign, s) : __int_as_float(0x7fffffff);
     }
 };
 
 // The codes of eight values, as two words.  x / s is formed as x fl(1/s),
 // within 2^-15 of the quotient for |x / s| <= 128, and rounded by adding
 // 1.5 2^23; where the product lies within 2^-13 of a half-integer (or is not
-// finite) the IEEE quotient decides.  (Elsewhere no code passes 127: the
-// largest value over a normal s is within 2^-16 of 127.)
-__device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], const RowScale &rs) {
+// finite) the IEEE quotient decides.  (Elsewhere no code passes 127: the largest value over a
+// normal s is within 2^-16 of 127.)
+template <int kSrc>
+__device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], const RowScale<kSrc> &rs) {
     constexpr float kMagic = 12582912.0f;
     if (!(rs.s > 0.0f)) return make_uint2(0u, 0u);
     const uint64_t magic = f32x2(kMagic, kMagic), inv = f32x2(rs.inv, rs.inv);
@@ -143,11 +146,12 @@ __device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], const RowScale &
         b[2 * i + 1] = __float_as_uint(tv.y);
     }
     if (!safe) {
+        const float s = RowScale<kSrc>::kSign * rs.s;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 v = f32x2_parts(f[i]);
-            b[2 * i] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(v.x, rs.s), -127.0f), 127.0f), kMagic));
-            b[2 * i + 1] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(v.y, rs.s), -127.0f), 127.0f), kMagic));
+            b[2 * i] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(v.x, s), -127.0f), 127.0f), kMagic));
+            b[2 * i + 1] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(v.y, s), -127.0f), 127.0f), kMagic));
         }
     }
     uint2 out;
@@ -196,9 +200,15 @@ template <int TPR>
 constexpr int kBlock = TPR == 32 ? 256 : TPR;
 
 // V > 0: the row's K <= 8 TPR V values stay in registers.  V == 0: any K,
-// the row is read twice (the second time from the caches).
-template <int kSrc, int TPR, int V>
-__global__ void __launch_bounds__(kBlock<TPR>) quantize_tokens_kernel(const __grid_constant__ Params p) {
+// the row is read twice (the second time from the caches).  kFirst: all of a
+// thread's loads are issued before any arithmetic, which pays for the SwiGLU's
+// long arithmetic with few rows or very many (128 x 13696: 6.2 -> 4.4 us, 2048
+// x 13696: 47.2 -> 40.8) and not where its registers cost a wave of blocks (512
+// x 13696: 12.6 -> 15.1; the plain quantizer, 4096 x 13696 fp16: 35.8 -> 45.7).
+// Rows brought ahead into shared memory by a producer thread were no faster
+// (2048 x 13696: 44.6): the issue of instructions, 29 a value, is the bound.
+template <int kSrc, int TPR, int V, bool kFirst>
+__global__ void __launch_bounds__(kBlock<TPR>, kFirst && TPR == 256 && V >= 5 && V <= 7 ? 3 : 0) quantize_tokens_kernel(const __grid_constant__ Params p) {
     __shared__ float sh_max[TPR / 32];
     __shared__ int sh_sum[TPR / 32];
     pdl_launch_dependents();
@@ -212,22 +222,42 @@ __global__ void __launch_bounds__(kBlock<TPR>) quantize_tokens_kernel(const __gr
     int sum = 0;
     if constexpr (V > 0) {
         uint64_t f[V][4];
+        if constexpr (kFirst) {
+            static_assert(kSrc == kSwiglu, "long arithmetic");
+            const uint16_t *src = static_cast<const uint16_t *>(p.X) + row * p.ldx + k0;
+            uint4 g[V], u[V];
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-            if (k0 + c * kStep < p.K) {
-                load8<kSrc>(p, row, k0 + c * kStep, f[c]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[c][i] = 0;
+            for (int c = 0; c < V; ++c) {
+                if (k0 + c * kStep < p.K) {
+                    g[c] = __ldg(reinterpret_cast<const uint4 *>(src + c * kStep));
+                    u[c] = __ldg(reinterpret_cast<const uint4 *>(src + p.K + c * kStep));
+                }
             }
-        }
 #pragma unroll
-        for (int c = 0; c < V; ++c) amax = max_abs(f[c], amax);
-        const RowScale rs(row_max<TPR>(amax, sh_max));
+            for (int c = 0; c < V; ++c) {
+                if (k0 + c * kStep < p.K) {
+                    swiglu8(g[c], u[c], f[c]);
+                    amax = max_abs(f[c], amax);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                if (k0 + c * kStep < p.K) {
+                    load8<kSrc>(p, row, k0 + c * kStep, f[c]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[c][i] = 0;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < V; ++c) amax = max_abs(f[c], amax);
+        }
+        const RowScale<kSrc> rs(row_max<TPR>(amax, sh_max));
 #pragma unroll
         for (int c = 0; c < V; ++c) {
             if (k0 + c * kStep < p.K) {
-                const uint2 w = codes8(f[c], rs);
+                const uint2 w = codes8<kSrc>(f[c], rs);
                 *reinterpret_cast<uint2 *>(dst + k0 + c * kStep) = w;
                 sum = __dp4a((int)w.x, 0x01010101, __dp4a((int)w.y, 0x01010101, sum));
             }
@@ -243,10 +273,10 @@ __global__ void __launch_bounds__(kBlock<TPR>) quantize_tokens_kernel(const __gr
             load8<kSrc>(p, row, k, f);
             amax = max_abs(f, amax);
         }
-        const RowScale rs(row_max<TPR>(amax, sh_max));
+        const RowScale<kSrc> rs(row_max<TPR>(amax, sh_max));
         for (int64_t k = k0; k < p.K; k += kStep) {
             load8<kSrc>(p, row, k, f);
-            const uint2 w = codes8(f, rs);
+            const uint2 w = codes8<kSrc>(f, rs);
             *reinterpret_cast<uint2 *>(dst + k) = w;
             sum = __dp4a((int)w.x, 0x01010101, __dp4a((int)w.y, 0x01010101, sum));
         }

@@ -23,7 +23,7 @@ inline size_t span(int64_t rows, int64_t pitch, int64_t width, size_t elem) {
 }
 
 // ---------------------------------------------------------------- per-token quantization
-template <int kSrc, int TPR, int V>
+template <int kSrc, int TPR, int V, bool kFirst>
 int launch_tokens_as(const tokens::Params &p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(TPR == 32 ? cdiv(p.M, 8) : p.M), 1, 1);
@@ -34,45 +34,52 @@ int launch_tokens_as(const tokens::Params &p, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, tokens::quantize_tokens_kernel<kSrc, TPR, V>, p) != cudaSuccess) return cuda_fail();
+    if (cudaLaunchKernelEx(&cfg, tokens::quantize_tokens_kernel<kSrc, TPR, V, kFirst>, p) != cudaSuccess) return cuda_fail();
     return launch_status();
 }
 
 // A row by one warp up to 1024 elements, by 256 threads up to 16384 where
 // there are rows enough to fill the GPU, else by 512 (a row's latency counts);
 // longer rows are read twice.
+template <int kSrc, bool kFirst>
+int launch_tokens_256(const tokens::Params &p, cudaStream_t st) {
+    switch (cdiv(p.K, 2048)) {
+        case 1: return launch_tokens_as<kSrc, 256, 1, kFirst>(p, st);
+        case 2: return launch_tokens_as<kSrc, 256, 2, kFirst>(p, st);
+        case 3: return launch_tokens_as<kSrc, 256, 3, kFirst>(p, st);
+        case 4: return launch_tokens_as<kSrc, 256, 4, kFirst>(p, st);
+        case 5: return launch_tokens_as<kSrc, 256, 5, kFirst>(p, st);
+        case 6: return launch_tokens_as<kSrc, 256, 6, kFirst>(p, st);
+        case 7: return launch_tokens_as<kSrc, 256, 7, kFirst>(p, st);
+        default: return launch_tokens_as<kSrc, 256, 8, kFirst>(p, st);
+    }
+}
+
+template <int kSrc, int V>
+int launch_tokens_512(DeviceInfo *d, const tokens::Params &p, cudaStream_t st) {
+    if constexpr (kSrc == tokens::kSwiglu)
+        if (p.M <= 2 * d->sms) return launch_tokens_as<kSrc, 512, V, true>(p, st);
+    return launch_tokens_as<kSrc, 512, V, false>(p, st);
+}
+
 template <int kSrc>
 int launch_tokens(DeviceInfo *d, const tokens::Params &p, cudaStream_t st) {
-#ifndef W8_TOK_ROWS
-#define W8_TOK_ROWS 4
-#endif
-    const bool many = p.M > W8_TOK_ROWS * d->sms;
+    constexpr bool kLong = kSrc == tokens::kSwiglu;     // long arithmetic: loads first
+    const bool many = p.M > 4 * d->sms;
     if (p.K <= 1024 && (many || p.K <= 256)) {
         switch (cdiv(p.K, 256)) {
-            case 1: return launch_tokens_as<kSrc, 32, 1>(p, st);
-            case 2: return launch_tokens_as<kSrc, 32, 2>(p, st);
-            default: return launch_tokens_as<kSrc, 32, 4>(p, st);
+            case 1: return launch_tokens_as<kSrc, 32, 1, false>(p, st);
+            case 2: return launch_tokens_as<kSrc, 32, 2, false>(p, st);
+            default: return launch_tokens_as<kSrc, 32, 4, false>(p, st);
         }
     }
-    if (many) {
-        switch (cdiv(p.K, 2048)) {
-            case 1: return launch_tokens_as<kSrc, 256, 1>(p, st);
-            case 2: return launch_tokens_as<kSrc, 256, 2>(p, st);
-            case 3: return launch_tokens_as<kSrc, 256, 3>(p, st);
-            case 4: return launch_tokens_as<kSrc, 256, 4>(p, st);
-            case 5: return launch_tokens_as<kSrc, 256, 5>(p, st);
-            case 6: return launch_tokens_as<kSrc, 256, 6>(p, st);
-            case 7: return launch_tokens_as<kSrc, 256, 7>(p, st);
-            case 8: return launch_tokens_as<kSrc, 256, 8>(p, st);
-            default: break;
-        }
-    }
+    if (p.K <= 16384 && p.M > (kLong ? 6 : 4) * d->sms) return launch_tokens_256<kSrc, kLong>(p, st);
     switch (cdiv(p.K, 4096)) {
-        case 1: return launch_tokens_as<kSrc, 512, 1>(p, st);
-        case 2: return launch_tokens_as<kSrc, 512, 2>(p, st);
+        case 1: return launch_tokens_512<kSrc, 1>(d, p, st);
+        case 2: return launch_tokens_512<kSrc, 2>(d, p, st);
         case 3:
-        case 4: return launch_tokens_as<kSrc, 512, 4>(p, st);
-        default: return launch_tokens_as<kSrc, 512, 0>(p, st);
+        case 4: return launch_tokens_512<kSrc, 4>(d, p, st);
+        default: return launch_tokens_as<kSrc, 512, 0, false>(p, st);
     }
 }
 

@@ -21,7 +21,8 @@ def _check(X, got):
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
 @pytest.mark.parametrize("M,K", [(1, 8), (1, 4096), (7, 24), (9, 504), (8, 512), (65, 520), (33, 1000), (17, 1024),
                                  (3, 2048), (5, 4096), (4, 4104), (2, 8192), (3, 13696), (2, 16384), (2, 16392),
-                                 (3, 40000), (1000, 64), (300, 768)])
+                                 (3, 40000), (1000, 64), (300, 768), (1001, 1032), (700, 4096), (449, 13696),
+                                 (601, 16384), (460, 16400)])
 def test_codes_scales_sums(M, K, dtype):
     rng = np.random.default_rng(M * 100003 + K)
     X = rng.normal(0, 1, (M, K)) * np.where(rng.random(K) < 0.01, 10, 1)
@@ -108,7 +109,8 @@ def test_no_rows():
     assert q.shape == (0, 64) and s.shape == (0,) and sums.shape == (0,)
 
 
-@pytest.mark.parametrize("M,K", [(1, 8), (5, 264), (3, 512), (16, 1000), (4, 4096), (16, 13696), (2, 16400), (200, 344)])
+@pytest.mark.parametrize("M,K", [(1, 8), (5, 264), (3, 512), (16, 1000), (4, 4096), (16, 13696), (2, 16400), (200, 344),
+                                 (1001, 1032), (700, 4096), (449, 13696), (450, 16384)])
 def test_swiglu(M, K):
     rng = np.random.default_rng(M * 7 + K)
     H = rng.normal(0, 2, (M, 2 * K)).astype(np.float16)
