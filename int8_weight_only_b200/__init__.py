@@ -508,21 +508,22 @@ def _call(fn, what, device, stream, *args):
         raise W8Error(rc, what)
 
 
-def _token_outputs(M, K, device, q, scales, sums):
+def _token_outputs(X, M, K, q, scales, sums):
     torch = _torch()
+    device = X.device
     if q is None:
-        q = torch.empty((M, _pitch(K)), dtype=torch.int8, device=device)
+        q = X.new_empty((M, _pitch(K)), dtype=torch.int8)
         if K % 16:
             q = q[:, :K]
     elif q.dtype != torch.int8 or q.shape != (M, K) or q.device != device:
         raise ValueError(f"q must be {(M, K)} int8 on {device}")
     ldq = _rows(q, "q") if M > 1 else _pitch(K)
     if scales is None:
-        scales = torch.empty((M,), dtype=torch.float32, device=device)
+        scales = X.new_empty((M,), dtype=torch.float32)
     else:
         _need(scales, "scales", torch.float32, (M,), device)
     if sums is None:
-        sums = torch.empty((M,), dtype=torch.int32, device=device)
+        sums = X.new_empty((M,), dtype=torch.int32)
     else:
         _need(sums, "sums", torch.int32, (M,), device)
     return q, ldq, scales, sums
@@ -547,7 +548,7 @@ def quantize_tokens(X, q=None, scales=None, sums=None):
         raise ValueError("X must be float32 or float16")
     M, K = X.shape
     dev = X.device
-    q, ldq, scales, sums = _token_outputs(M, K, dev, q, scales, sums)
+    q, ldq, scales, sums = _token_outputs(X, M, K, q, scales, sums)
     _call(lib.w8_quantize_per_token, "w8_quantize_per_token", dev, _raw_stream(dev), X.data_ptr(), dt, ldx, M, K,
           q.data_ptr(), ldq, scales.data_ptr(), sums.data_ptr())
     return q, scales, sums
@@ -564,7 +565,7 @@ def swiglu_quantize_tokens(H, q=None, scales=None, sums=None):
         raise ValueError("H must be [M, 2K] float16")
     M, K = H.shape[0], H.shape[1] // 2
     dev = H.device
-    q, ldq, scales, sums = _token_outputs(M, K, dev, q, scales, sums)
+    q, ldq, scales, sums = _token_outputs(H, M, K, q, scales, sums)
     _call(lib.w8_swiglu_quantize_per_token, "w8_swiglu_quantize_per_token", dev, _raw_stream(dev), H.data_ptr(), ldh,
           M, K, q.data_ptr(), ldq, scales.data_ptr(), sums.data_ptr())
     return q, scales, sums
@@ -591,7 +592,7 @@ def _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, lead):
     if zeros is not None:
         _need(zeros, "zeros", torch.int8, lead + (N,), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=dev)
+        out = q.new_empty((M, N), dtype=torch.float16)
     else:
         _need(out, "out", torch.float16, (M, N), dev)
     return ldq, M, K, N, out
