@@ -312,3 +312,53 @@ def test_refusals():
                       ("scales", scales), ("packed", packed), ("bias", b), ("zeros", zeros)]:
         with pytest.raises(ValueError):
             m.linear_w8a8_grouped(**{**grouped, name: bad})
+
+
+def _log_size(rng, lo, hi, step=1):
+    return max(step, int(round(np.exp(rng.uniform(np.log(lo), np.log(hi))) / step)) * step)
+
+
+@pytest.mark.parametrize("seed", range(48))
+def test_linear_random_sizes(seed):
+    # every kernel and the borders between them
+    rng = np.random.default_rng(1000 + seed)
+    while True:
+        M, K, N = _log_size(rng, 1, 3000), _log_size(rng, 8, 9000, 8), _log_size(rng, 8, 24000, 8)
+        if M * K * N <= 3e9:
+            break
+    ops = operands(M, K, N, seed, asym=bool(rng.integers(2)), bias=bool(rng.integers(2)))
+    _check(ops, _run(ops), f"M={M} K={K} N={N}")
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_grouped_random_sizes(seed):
+    rng = np.random.default_rng(2000 + seed)
+    E, K, N = _log_size(rng, 1, 40), _log_size(rng, 8, 2000, 8), _log_size(rng, 8, 3000, 8)
+    most = max(1, int(min(1500, 2e9 / (K * N))))
+    share = rng.dirichlet(np.full(E, 0.5))
+    counts = rng.multinomial(rng.integers(1, most + 1), share).tolist()
+    _grouped(counts, K, N, seed, before=int(rng.integers(0, 4)), behind=int(rng.integers(0, 300)),
+             asym=bool(rng.integers(2)), bias=bool(rng.integers(2)))
+
+
+def test_two_streams_at_once():
+    # calls of every kernel, eagerly on two streams that overlap on the GPU
+    import torch
+    m = w8()
+    shapes = [(1, 4096, 4096), (40, 1024, 16384), (200, 4096, 1024), (700, 1024, 4096), (5, 13696, 1024)]
+    ops = [operands(M, K, N, i) for i, (M, K, N) in enumerate(shapes)]
+    args = [(pitched(torch, o[0]), _gpu(o[1]), _gpu(o[2]), m.prepack(_gpu(o[3])), _gpu(o[4])) for o in ops]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for turn in range(20):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append([m.linear_w8a8(*a) for a in args])
+    torch.cuda.synchronize()
+    first = [to_np(y) for y in outs[0]]
+    for y, o in zip(outs[0], ops):
+        _check(o, y)
+    for got in outs[1:]:
+        assert all(np.array_equal(to_np(y), f) for y, f in zip(got, first))
+    assert m.device_status() == 0
