@@ -371,6 +371,9 @@ int w8a8_linear(const int8_t *q, int64_t ldq, const float *x_scales, const int32
  *   packed    [groups] w8_prepack outputs, one after another; scales, zeros
  *             and bias [groups, N].
  *   1 <= groups <= 1024, M <= 2^24.
+ * Kernel choice (internal, by the mean group): single SMs with tiles of 16 or
+ *   32 tokens for few, pairs of SMs with tiles of 128 or 256 for many; any
+ *   groups are computed whichever it is.
  * Other arguments, results and errors as w8a8_linear.
  */
 int w8a8_linear_grouped(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums,

@@ -17,12 +17,15 @@
 // workspace, took 21.7 us against 20.0 for 1 x 4096 x 27392 (107 blocks with
 // two tiles each), 14.7 against 12.0 for 1 x 4096 x 13696 and 31.4 against 29.0
 // for 1 x 13696 x 12000.  Fewer than half as many output tiles as SMs go to
-// clusters (w8a8_cluster.cuh).
+// clusters (w8a8_cluster.cuh).  Groups of few tokens (kGrouped) run here too,
+// their tiles counted on the device (8 groups of 2 x 4096 x 4096: 21.3 us).
 //
 // Roles: warp 0 producer (weight tiles by one bulk copy, tokens by TMA),
 // warp 1 issues the products, warp 2 owns the tensor memory, warps 4 and up
 // scale and store.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -71,6 +74,88 @@ struct Params {
     int KB;                    // ceil(K / 64)
 };
 
+constexpr int kMaxGroups = 1024;
+// The groups' rows and token tiles, in shared memory.
+struct Groups {
+    int first[kMaxGroups + 1];    // first row, within [0, rows]
+    int tiles[kMaxGroups + 1];    // token tiles of all groups before
+};
+struct OneGroup {};
+
+// All kThreads_ threads of the block; a block barrier has to follow.  The
+// first rows are clamped to [0, rows], so no offset can lead out of bounds.
+template <int TN, int kThreads_>
+__device__ __forceinline__ void load_groups(const Params &p, Groups &g) {
+    for (int e = threadIdx.x; e <= p.groups; e += kThreads_) g.first[e] = (int)max64(0, min64(p.rows, p.offsets[e]));
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int before = 0;
+        if (lane == 0) g.tiles[0] = 0;
+        for (int e0 = 0; e0 < p.groups; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < p.groups) n = (max(0, g.first[e + 1] - g.first[e]) + TN - 1) / TN;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, n, d);
+                if (lane >= d) n += o;
+            }
+            if (e < p.groups) g.tiles[e + 1] = before + n;
+            before += __shfl_sync(0xffffffffu, n, 31);
+        }
+    }
+}
+
+// Output tiles dealt round robin to as few blocks as keep the longest run of
+// tiles short: equally many each draw the weights evenly.  One group: tile u is
+// channel block u / tt_n, token tile u % tt_n.  Several: those of a group
+// follow one another.
+struct Tile {
+    int group, nb;
+    int64_t row0;
+    int rows;
+};
+template <int TN, bool kGrouped>
+struct Deal {
+    const Params &p;
+    const Groups *g;
+    int u, units, step, group;
+    __device__ Deal(const Params &p_, const Groups *groups) : p(p_), g(groups), u(blockIdx.x), group(0) {
+        // the host keeps the tiles of a call below 2^31, whatever overlapping
+        // groups would add up to
+        const int64_t all = kGrouped ? (int64_t)groups->tiles[p.groups] * p.NB : (p.rows + TN - 1) / TN * p.NB;
+        units = (int)min64(all, INT32_MAX / 2);
+        step = gridDim.x;
+        if constexpr (kGrouped) {
+            // (the host has sized the grid so where it knows the tiles)
+            const unsigned each = ((unsigned)units + gridDim.x - 1) / gridDim.x;
+            if (each > 0) step = (int)(((unsigned)units + each - 1) / each);
+            if (u >= step) u = units;
+        }
+    }
+    __device__ bool next(Tile &t) {
+        if (u >= units) return false;
+        int local = u, tt_n;
+        int64_t first = 0, end = p.rows;
+        if constexpr (kGrouped) {
+            while ((int64_t)u >= (int64_t)p.NB * g->tiles[group + 1]) ++group;
+            local -= p.NB * g->tiles[group];
+            tt_n = g->tiles[group + 1] - g->tiles[group];
+            first = g->first[group];
+            end = g->first[group + 1];
+        } else {
+            tt_n = (int)((p.rows + TN - 1) / TN);
+        }
+        t.group = group;
+        t.nb = local / tt_n;
+        t.row0 = first + (int64_t)(local - t.nb * tt_n) * TN;
+        t.rows = (int)min64(TN, end - t.row0);
+        u += step;
+        return true;
+    }
+};
+
 // The outputs of C tokens (columns) of this thread's channel, as pairs of
 // tokens: y = s_m s_n (sum - off sum_m) + bias, rounded once to fp16.  sums
 // and x_scales (shared memory, 16-byte aligned) belong to the tokens.
@@ -111,7 +196,7 @@ __device__ __forceinline__ void store_tokens(const uint32_t (&v)[C], const int *
     }
 }
 
-template <int TN>
+template <int TN, bool kGrouped>
 __global__ void __launch_bounds__(Cfg<TN>::kThreads, 1)
 w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ Params p) {
     using C = Cfg<TN>;
@@ -123,6 +208,8 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
     __shared__ uint32_t tmem_base_sh;
     __shared__ __align__(16) int sum_sh[2][TN];       // the token tile's sums and scales
     __shared__ __align__(16) float xs_sh[2][TN];
+    using GroupsSh = typename std::conditional<kGrouped, Groups, OneGroup>::type;
+    __shared__ GroupsSh groups_sh;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // warp-uniform
     const int lane = threadIdx.x & 31;
@@ -144,15 +231,17 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
         tmem_relinquish();
     }
     pdl_launch_dependents();
-    // Output tile u: channel block u / tt_n, token tile u % tt_n.
-    const int tt_n = (int)((p.rows + TN - 1) / TN);
-    const int64_t units = (int64_t)tt_n * p.NB;
-    auto weights_of = [&](int64_t u) { return p.packed + u / tt_n * p.KB * kTile; };
-    auto row_of = [&](int64_t u) { return (int64_t)(u % tt_n) * TN; };
-    if (threadIdx.x == 0 && blockIdx.x < units) {
+    const Groups *groups = nullptr;
+    if constexpr (kGrouped) {
+        pdl_wait();
+        load_groups<TN, C::kThreads>(p, *reinterpret_cast<Groups *>(&groups_sh));
+        groups = reinterpret_cast<const Groups *>(&groups_sh);
+    } else if (threadIdx.x == 0) {
         // the first weights into L2 while the previous kernel ends; they are
         // never stale there, whoever writes them
-        prefetch_l2(weights_of(blockIdx.x), (uint32_t)min(p.KB, kPrefetch) * kTile);
+        Deal<TN, false> deal(p, nullptr);
+        Tile t;
+        if (deal.next(t)) prefetch_l2(p.packed + (int64_t)t.nb * p.KB * kTile, (uint32_t)min(p.KB, kPrefetch) * kTile);
     }
     tc_fence_before();
     __syncthreads();
@@ -166,9 +255,10 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
             int st = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const uint8_t *w = weights_of(u);
-                const int row0 = (int)row_of(u);
+            Deal<TN, kGrouped> deal(p, groups);
+            Tile t;
+            while (ok && deal.next(t)) {
+                const uint8_t *w = p.packed + ((int64_t)t.group * p.NB + t.nb) * p.KB * kTile;
                 for (int kb = 0; kb < p.KB; kb += kStep) {
                     const int cnt = min(kStep, p.KB - kb), boxes = (cnt + 1) >> 1;
                     if (!mbar_wait(&empty[st], ph ^ 1u, SITE_I8_EMPTY)) { ok = false; break; }
@@ -176,7 +266,7 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
                     mbar_arrive_expect_tx(&full[st], cnt * kTile + boxes * C::kXBox);
                     bulk_g2s(ws, w + (int64_t)kb * kTile, cnt * kTile, &full[st]);
                     for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(xs + b * C::kXBox, &tmap_x, (kb + 2 * b) * 64, row0, &full[st]);
+                        tma_load_2d(xs + b * C::kXBox, &tmap_x, (kb + 2 * b) * 64, (int)t.row0, &full[st]);
                     ++issued;
                     if (++st == C::kStages) { st = 0; ph ^= 1u; }
                 }
@@ -196,8 +286,10 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
         bool ok = true;
         const uint64_t w_desc0 = smem_desc_kmajor_sw64(smem_u32(ring));
         const uint64_t x_desc0 = smem_desc_kmajor_sw128(smem_u32(ring) + kWBytes);
-        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const int n = ((int)min64(TN, p.rows - row_of(u)) + 15) & ~15;
+        Deal<TN, kGrouped> deal(p, groups);
+        Tile tile;
+        while (ok && deal.next(tile)) {
+            const int n = (tile.rows + 15) & ~15;
             const uint32_t idesc = idesc_u8_s8_s32(kBN, n);
             const uint32_t dst = tmem + d * TN;
             if (!warp_all(mbar_wait(&d_empty[d], dph ^ 1u, SITE_I8_DEMPTY))) { ok = false; break; }
@@ -244,14 +336,17 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
         const int cb = C::kEpiTokens * ((warp - 4) >> 2);     // this warp's first token
         int d = 0;
         uint32_t dph = 0;
-        for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-            const int64_t row0 = row_of(u);
-            const int nr = (int)min64(TN, p.rows - row0);
-            const int64_t n = u / tt_n * kBN + r;
+        Deal<TN, kGrouped> deal(p, groups);
+        Tile tile;
+        while (deal.next(tile)) {
+            const int64_t row0 = tile.row0;
+            const int nr = tile.rows;
+            const int64_t n = (int64_t)tile.nb * kBN + r;
             const bool n_ok = n < p.N;
-            const float sc = n_ok ? __half2float(__ushort_as_half(p.scales[n])) : 0.0f;
-            const float bi = (n_ok && p.bias) ? __half2float(__ushort_as_half(p.bias[n])) : 0.0f;
-            const int off = 128 + ((n_ok && p.zeros) ? (int)p.zeros[n] : 0);
+            const int64_t ch = (int64_t)tile.group * p.N + n;
+            const float sc = n_ok ? __half2float(__ushort_as_half(p.scales[ch])) : 0.0f;
+            const float bi = (n_ok && p.bias) ? __half2float(__ushort_as_half(p.bias[ch])) : 0.0f;
+            const int off = 128 + ((n_ok && p.zeros) ? (int)p.zeros[ch] : 0);
             // the tokens' sums and scales, read while the products run; the
             // other buffer may still be read for the tile before
             if (const int c = threadIdx.x - 128; c < TN) {

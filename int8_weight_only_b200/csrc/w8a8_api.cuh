@@ -206,7 +206,7 @@ int launch_w8a8_as(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, w8a8::w8a8_kernel<TN>, map, p) != cudaSuccess) return cuda_fail();
+    if (cudaLaunchKernelEx(&cfg, w8a8::w8a8_kernel<TN, false>, map, p) != cudaSuccess) return cuda_fail();
     return launch_status();
 }
 
@@ -286,11 +286,39 @@ int launch_w8a8(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8
     return launch_w8a8_pair<256, false>(d, q, ldq, K, p, st);
 }
 
+// Groups on single SMs (w8a8.cuh): one block each, the kernel deals the tiles.
+template <int TN>
+int launch_w8a8_groups(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
+    if ((cdiv(p.rows, TN) + p.groups) * p.NB > INT32_MAX / 2) return W8_ERR_SHAPE;   // tile numbers are 32-bit
+    CUtensorMap map;
+    const int rc = make_map_codes(&map, q, ldq, p.rows, K, TN);
+    if (rc != W8_OK) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)d->sms, 1, 1);
+    cfg.blockDim = dim3(w8a8::Cfg<TN>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = w8a8::Cfg<TN>::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, w8a8::w8a8_kernel<TN, true>, map, p) != cudaSuccess) return cuda_fail();
+    return launch_status();
+}
+
 // The kernel of a grouped product, by the mean group (the groups themselves
-// are known on the device only): tiles of 256 tokens from 96 tokens on.  8
-// groups of 4096 x 4096, microseconds with tiles of 128 / 256: 16 tokens each
-// 24.6 / 25.9, 64 25.9 / 27.6, 128 31.2 / 30.2, 256 46.0 / 40.0.
+// are known on the device only).  Up to 4 tokens, and up to 16 where the
+// products are long enough to hide its stores, single SMs with tiles of 16 and
+// 32 tokens; else pairs of SMs, with tiles of 256 tokens from 96 tokens on.
+// Microseconds with tiles of 16 / 32 on single SMs, 128 / 256 on pairs, 8
+// groups of 4096 x 4096: 2 tokens each 21.3 / 21.7, 23.5 / -, 8 23.0 / 23.4,
+// 24.0 / -, 16 25.6 / 23.7, 24.3 / 25.9, 64 54.6 / 37.2, 25.7 / 27.6, 128 - / -,
+// 31.2 / 30.2, 256 - / -, 46.0 / 40.0; 39 groups of 288 x 11040, 23 tokens each:
+// 53.4 / 50.7, 33.0 / 33.2.
 int launch_w8a8_grouped(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
+    if (p.rows <= 4 * (int64_t)p.groups) return launch_w8a8_groups<16>(d, q, ldq, K, p, st);
+    if (p.rows <= 16 * (int64_t)p.groups && K >= 1024) return launch_w8a8_groups<32>(d, q, ldq, K, p, st);
     if (p.rows > 96 * (int64_t)p.groups) return launch_w8a8_pair<256, true>(d, q, ldq, K, p, st);
     return launch_w8a8_pair<128, true>(d, q, ldq, K, p, st);
 }
@@ -308,13 +336,19 @@ cudaError_t w8a8_attributes() {
 #undef W8_I8_CLUSTER_SMEM
 #define W8_I8_SMEM(TN)                                                                                        \
     if (e == cudaSuccess)                                                                                     \
-        e = cudaFuncSetAttribute((const void *)w8a8::w8a8_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
+        e = cudaFuncSetAttribute((const void *)w8a8::w8a8_kernel<TN, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
                                  w8a8::Cfg<TN>::kSmemBytes);
     W8_I8_SMEM(16)
     W8_I8_SMEM(32)
     W8_I8_SMEM(64)
     W8_I8_SMEM(128)
 #undef W8_I8_SMEM
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute((const void *)w8a8::w8a8_kernel<16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 w8a8::Cfg<16>::kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute((const void *)w8a8::w8a8_kernel<32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 w8a8::Cfg<32>::kSmemBytes);
 #define W8_I8_PAIR_SMEM(BT)                                                                                   \
     for (const void *f : {(const void *)w8a8::pair::w8a8_pair_kernel<BT, false>,                             \
                           (const void *)w8a8::pair::w8a8_pair_kernel<BT, true>})                              \
@@ -334,7 +368,7 @@ int w8a8_common(const int8_t *q, int64_t ldq, const float *x_scales, const int32
     if (M < 0 || K < 1 || N < 1 || K % 8 != 0 || N % 8 != 0 || K > kMaxSumK || M > (int64_t)INT32_MAX - 512 ||
         N > (1LL << 30) || ldq < K || ldq % 16 != 0 || ldq >= (1LL << 40))
         return W8_ERR_SHAPE;
-    if (grouped && (groups < 1 || groups > w8a8::pair::kMaxGroups || M > kMaxGroupedRows)) return W8_ERR_SHAPE;
+    if (grouped && (groups < 1 || groups > w8a8::kMaxGroups || M > kMaxGroupedRows)) return W8_ERR_SHAPE;
     if (!packed || !scales || (grouped && !offsets)) return W8_ERR_NULL;
     if (M == 0) return W8_OK;   // no rows: nothing to read or write
     if (!q || !x_scales || !x_sums || !Y) return W8_ERR_NULL;

@@ -158,6 +158,13 @@ def test_grouped(counts, K, N):
     _grouped(counts, K, N, n + K, before=n % 3, behind=(n % 5) * 7, asym=n % 2 == 0, bias=n % 3 == 0)
 
 
+@pytest.mark.parametrize("mean", [4, 5, 16, 17, 96, 97])
+def test_grouped_kernel_borders(mean):
+    # mean groups on both sides of each border, one group with most of the rows
+    for counts in ([mean] * 3, [0, 3 * mean - 1, 1], [3 * mean, 0, 0]):
+        _grouped(counts, 1032, 264, mean, asym=mean % 2 == 0, bias=True)
+
+
 def test_grouped_many_groups():
     rng = np.random.default_rng(1)
     _grouped(list(rng.integers(0, 4, 1024)), 64, 128, 21, behind=3, bias=True)
