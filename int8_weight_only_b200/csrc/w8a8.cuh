@@ -1,6 +1,6 @@
 // W8A8 linear: Y[m,n] = s_m s_n sum_k x[m,k] (w[k,n] - z_n) + bias_n with int8
 // activations x (scale s_m per token) and int8 weights w (scale s_n and zero
-// point z_n per channel), one weight or one per group of tokens (experts).
+// point z_n per channel), one weight or one for each group of tokens (experts).
 //
 // The packed weight tile holds the bytes u = w + 128 of 128 channels x 64
 // features as rows of 64 bytes in the 64-byte-swizzle order, so a tile copied
@@ -11,7 +11,8 @@
 // and sum_k x, one integer per token, comes with the activations.
 //
 // This kernel: few tokens, whole output tiles of 128 channels x TN tokens dealt
-// round robin to the thread blocks.  It is bound by the weight stream, which
+// round robin to the thread blocks.  It is bound by the weight stream (1 x 4096
+// x 27392: 18.4 us, 6.1 TB/s, 93 % of the measured copy rate), which
 // 94 of 148 SMs already draw at 5.7 TB/s, so sharing output tiles to occupy
 // all SMs does not pay: an even split over K, the parts added through the
 // workspace, took 21.7 us against 20.0 for 1 x 4096 x 27392 (107 blocks with
