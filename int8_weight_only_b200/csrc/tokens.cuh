@@ -12,7 +12,7 @@
 // of instructions, 28 a value (2048 x 13696: 40.7 us, 3.4 TB/s).
 #pragma once
 
-#include "common.cuh"
+#include "i8.cuh"
 
 namespace w8 {
 namespace tokens {

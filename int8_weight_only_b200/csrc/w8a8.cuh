@@ -28,7 +28,7 @@
 
 #include <type_traits>
 
-#include "common.cuh"
+#include "i8.cuh"
 
 namespace w8 {
 namespace w8a8 {
