@@ -517,7 +517,9 @@ def _token_outputs(X, M, K, q, scales, sums):
             q = q[:, :K]
     elif q.dtype != torch.int8 or q.shape != (M, K) or q.device != device:
         raise ValueError(f"q must be {(M, K)} int8 on {device}")
-    ldq = _rows(q, "q") if M > 1 else _pitch(K)
+    ldq = _rows(q, "q")
+    if M <= 1:
+        ldq = _pitch(K)
     if scales is None:
         scales = X.new_empty((M,), dtype=torch.float32)
     else:
