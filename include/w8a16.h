@@ -303,7 +303,8 @@ int w8a16_linear_asym(const uint16_t *X, const uint8_t *packed, const uint16_t *
  *   q       [M, K] int8, rows ldq >= K bytes apart, ldq a multiple of 16.
  *           Bytes between K and ldq are neither read nor written anywhere.
  *   scales  [M] fp32;  sums  [M] int32.
- *   M >= 0 (0 is a no-op), K >= 1 with K % 8 == 0.  Inputs must be finite
+ *   M >= 0 (0 is a no-op); K >= 1 with K % 8 == 0 and K <= 16909320 (2^31 /
+ *   127: no sum of codes wraps).  Inputs must be finite
  *   (rows are independent: a row that is not spoils only itself).
  * Errors: W8_ERR_NULL, W8_ERR_SHAPE, W8_ERR_ALIGN, W8_ERR_DTYPE,
  *         W8_ERR_ALIAS, W8_ERR_DEVICE, W8_ERR_CUDA.

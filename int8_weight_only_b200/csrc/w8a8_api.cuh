@@ -12,6 +12,8 @@ namespace {
 
 // Sums of 128 x 255 x K must stay below 2^31.
 constexpr int64_t kMaxSumK = 65536;
+// So must the sum of a row's codes, 127 K at most.
+constexpr int64_t kMaxTokenK = INT32_MAX / 127;
 // Rows of a grouped call: the token tiles of 1024 groups stay below 2^31
 // whatever the offsets on the device are.
 constexpr int64_t kMaxGroupedRows = 1 << 24;
@@ -83,14 +85,12 @@ int launch_tokens(DeviceInfo *d, const tokens::Params &p, cudaStream_t st) {
     }
 }
 
-// x_cols: elements of a row that are read (K, or 2K for the SwiGLU).
 int tokens_common(const void *X, int dtype, bool swiglu, int64_t ldx, int64_t M, int64_t K, int8_t *q, int64_t ldq,
                   float *scales, int32_t *sums, void *stream) {
     if (dtype != W8_F32 && dtype != W8_F16) return W8_ERR_DTYPE;
-    const int64_t cols = swiglu ? 2 * K : K;
-    if (M < 0 || K < 1 || K % 8 != 0 || M > (int64_t)INT32_MAX || K > (int64_t)INT32_MAX / 2 || ldx < cols || ldq < K ||
-        ldq % 16 != 0 || ldx > (1LL << 40) || ldq > (1LL << 40))
-        return W8_ERR_SHAPE;
+    if (M < 0 || K < 1 || K % 8 != 0 || M > (int64_t)INT32_MAX || K > kMaxTokenK) return W8_ERR_SHAPE;
+    const int64_t cols = swiglu ? 2 * K : K;   // elements of a row that are read
+    if (ldx < cols || ldq < K || ldq % 16 != 0 || ldx > (1LL << 40) || ldq > (1LL << 40)) return W8_ERR_SHAPE;
     if (M == 0) return W8_OK;
     if (!X || !q || !scales || !sums) return W8_ERR_NULL;
     const size_t elem = dtype == W8_F32 ? 4 : 2;
