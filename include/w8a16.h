@@ -304,8 +304,11 @@ int w8a16_linear_asym(const uint16_t *X, const uint8_t *packed, const uint16_t *
  *           Bytes between K and ldq are neither read nor written anywhere.
  *   scales  [M] fp32;  sums  [M] int32.
  *   M >= 0 (0 is a no-op); K >= 1 with K % 8 == 0 and K <= 16909320 (2^31 /
- *   127: no sum of codes wraps).  Inputs must be finite
- *   (rows are independent: a row that is not spoils only itself).
+ *   127: no sum of codes wraps).
+ *   Rows are independent, and one that is not finite stays visible as such: a
+ *   NaN in it makes s_m NaN and all its codes 0; infinities alone make s_m
+ *   infinite, their codes +-127 by their sign and the others 0.  Every output
+ *   that w8a8_linear computes from such a row is NaN or infinite.
  * Errors: W8_ERR_NULL, W8_ERR_SHAPE, W8_ERR_ALIGN, W8_ERR_DTYPE,
  *         W8_ERR_ALIAS, W8_ERR_DEVICE, W8_ERR_CUDA.
  */
@@ -318,7 +321,8 @@ int w8_quantize_per_token(const void *X, int x_dtype, int64_t ldx, int64_t M, in
  * gate in its first K columns and the up projection in the others (the
  * ChatGLM2 h-to-4h output: 27392 = 2 x 13696),
  *   h[m,k] = g / (1 + exp(-g)) * u,  g = H[m,k], u = H[m,K+k]   in fp32,
- * then codes, scales and sums of h as w8_quantize_per_token.  Rows of H are
+ * then codes, scales and sums of h as w8_quantize_per_token.  (A gate of
+ * -infinity gives NaN, as this formula does in fp32.)  Rows of H are
  * ldh >= 2K elements apart.  Other arguments and errors as there.
  */
 int w8_swiglu_quantize_per_token(const uint16_t *H, int64_t ldh, int64_t M, int64_t K, int8_t *q, int64_t ldq,

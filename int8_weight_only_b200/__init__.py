@@ -537,7 +537,8 @@ def quantize_tokens(X, q=None, scales=None, sums=None):
     Rows of X may be strided (columns contiguous).  Returns (q int8 [M, K],
     scales fp32 [M], sums int32 [M], the sum of each row's codes).  The rows
     of q start on 16-byte boundaries: for K % 16 != 0 it is a view of a wider
-    buffer.
+    buffer.  A row with a NaN gets a NaN for its scale, a row with infinities
+    an infinite one, so that linear_w8a8's outputs of it are not finite either.
     """
     torch = _torch()
     lib = load_library()

@@ -5,6 +5,11 @@
 // MLP's first product, h = g / (1 + exp(-g)) * u.  The row sums let the
 // int8 linear undo the offset of the weight codes.
 //
+// What is not finite stays visible behind the linear.  A row with a NaN has a
+// NaN for its scale (and codes of 0): every output of the row is NaN.  A row
+// with infinities has an infinite scale, their codes at the last level of
+// their sign and the others 0: every output is infinite or NaN.
+//
 // One pass over X: a row is spread over TPR threads, each of which holds its
 // values in registers between the row maximum and the rounding, so the plain
 // quantizer is bound by HBM for many rows (4096 x 4096 fp32: 13.6 us, 6.2 TB/s)
@@ -125,6 +130,14 @@ struct RowScale {
     }
 };
 
+// The IEEE quotient v / (kSign s), clamped to the levels.  Of an infinity, whose
+// row has an infinite scale, the quotient is NaN, which fminf turns into the
+// last level.
+template <int kSrc>
+__device__ __forceinline__ float level(float v, float s) {
+    return copysignf(fminf(__fdiv_rn(fabsf(v), s), 127.0f), RowScale<kSrc>::kSign * v);
+}
+
 // The codes of eight values, as two words.  x / s is formed as x fl(1/s),
 // within 2^-15 of the quotient for |x / s| <= 128, and rounded by adding
 // 1.5 2^23; where the product lies within 2^-13 of a half-integer (or is not
@@ -133,7 +146,7 @@ struct RowScale {
 template <int kSrc>
 __device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], const RowScale<kSrc> &rs) {
     constexpr float kMagic = 12582912.0f;
-    if (!(rs.s > 0.0f)) return make_uint2(0u, 0u);
+    if (!(rs.s > 0.0f)) return make_uint2(0u, 0u);   // a row of zeros, or with a NaN
     const uint64_t magic = f32x2(kMagic, kMagic), inv = f32x2(rs.inv, rs.inv);
     uint32_t b[8];
     bool safe = true;
@@ -147,12 +160,11 @@ __device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], const RowScale<k
         b[2 * i + 1] = __float_as_uint(tv.y);
     }
     if (!safe) {
-        const float s = RowScale<kSrc>::kSign * rs.s;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 v = f32x2_parts(f[i]);
-            b[2 * i] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(v.x, s), -127.0f), 127.0f), kMagic));
-            b[2 * i + 1] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(v.y, s), -127.0f), 127.0f), kMagic));
+            b[2 * i] = __float_as_uint(__fadd_rn(level<kSrc>(v.x, rs.s), kMagic));
+            b[2 * i + 1] = __float_as_uint(__fadd_rn(level<kSrc>(v.y, rs.s), kMagic));
         }
     }
     uint2 out;
@@ -161,24 +173,36 @@ __device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], const RowScale<k
     return out;
 }
 
+// The largest of m, |a| and |b|; a NaN among them gives NaN (fmaxf would drop it).
+__device__ __forceinline__ float max_abs_nan(float m, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float max_abs(const uint64_t (&f)[4], float m) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 v = f32x2_parts(f[i]);
-        m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+        m = max_abs_nan(m, v.x, v.y);
     }
     return m;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 template <int TPR>
 __device__ __forceinline__ float row_max(float v, float *sh) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+    for (int d = 16; d > 0; d >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, d));
     if constexpr (TPR > 32) {
         if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < TPR / 32; ++i) v = fmaxf(v, sh[i]);
+        for (int i = 0; i < TPR / 32; ++i) v = max_nan(v, sh[i]);
     }
     return v;
 }
