@@ -908,6 +908,8 @@ int w8a16_linear_asym(const uint16_t *X, const uint8_t *packed, const uint16_t *
 namespace {
 __global__ void bounded_wait_selftest_kernel(unsigned long long limit_ns) {
     __shared__ uint64_t bar;
+    // the next kernel may start: what it waits for is this one's end
+    pdl_launch_dependents();
     if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
         fence_barrier_init();

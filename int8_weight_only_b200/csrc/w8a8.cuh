@@ -282,6 +282,7 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
         // ---------------------------------------------------- products
         // the whole warp walks the steps and one elected lane issues: the
         // operands stay in uniform registers
+        pdl_wait();   // before the first bounded wait: its second is this call's own
         int st = 0, d = 0;
         uint32_t ph = 0, dph = 0;
         bool ok = true;

@@ -113,6 +113,7 @@ w8a8_cluster_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_con
         }
     } else if (warp == 1) {
         // ---------------------------------------------------- products
+        pdl_wait();   // before the first bounded wait: its second is this call's own
         int st = 0;
         uint32_t ph = 0, acc = 0;
         const uint64_t w_desc0 = smem_desc_kmajor_sw64(smem_u32(ring));

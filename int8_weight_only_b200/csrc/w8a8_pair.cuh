@@ -213,6 +213,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
         // on the lane number a product took 256 cycles to issue instead of
         // the 128 it runs for (2048 x 4096 x 27392: 198 us).
         if (rank == 0) {
+            pdl_wait();   // before the first bounded wait: its second is this call's own
             int st = 0, d = 0;
             uint32_t ph = 0, dph = 0;
             bool ok = true;

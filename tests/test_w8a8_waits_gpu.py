@@ -1,0 +1,43 @@
+"""The bounded waits of the W8A8 kernels: their second begins when the kernel
+before has ended."""
+import pytest
+
+from tests.gpu_helpers import to_gpu, to_np, w8
+from tests.w8a8_helpers import assert_linear, linear, operands, pitched
+
+pytestmark = pytest.mark.gpu
+
+LONG_NS = 1_300_000_000     # more than a wait's one second
+
+
+# (M, K, N, groups): clusters of 8 and of 2, whole tiles on single SMs, pairs
+# of SMs with tiles of 128 and of 256 tokens, and the groups' three kernels
+@pytest.mark.parametrize("M,K,N,E", [(3, 4096, 256, 0), (100, 1024, 1024, 0), (5, 256, 16384, 0), (140, 1032, 4968, 0),
+                                     (520, 1032, 4968, 0), (6, 1024, 264, 3), (40, 1024, 264, 2), (300, 520, 264, 2)])
+def test_a_long_kernel_before_does_not_use_up_the_wait(M, K, N, E):
+    import torch
+    m = w8()
+    q, xs, sums, w, scales, zeros, b = operands(M, K, N, M + N, lead=(E,) if E else (), asym=True, bias=True)
+    args = [pitched(torch, q), to_gpu(xs), to_gpu(sums)]
+    tail = dict(bias=to_gpu(b), zeros=to_gpu(zeros), out=torch.full((M, N), 3.5, dtype=torch.float16, device="cuda"))
+    if E:
+        at = [M * e // E for e in range(E + 1)]
+        args += [torch.tensor(at, dtype=torch.int32, device="cuda"),
+                 torch.stack([m.prepack(to_gpu(w[e])) for e in range(E)]), to_gpu(scales)]
+        f = m.linear_w8a8_grouped
+    else:
+        args += [m.prepack(to_gpu(w)), to_gpu(scales)]
+        f = m.linear_w8a8
+    f(*args, **tail)
+    first = to_np(tail["out"])
+    tail["out"].fill_(3.5)
+    assert m.device_status() == 0
+    m.test_bounded_wait(LONG_NS)
+    got = f(*args, **tail)
+    # the one wait that ran out is that of the kernel before
+    assert (m.device_status() >> 8) & 0xFF == 0xEE
+    assert (to_np(got) == first).all()
+    for e in range(max(E, 1)):
+        r = slice(at[e], at[e + 1]) if E else slice(0, M)
+        i = e if E else ()
+        assert_linear(first[r], *linear(q[r], xs[r], w[i], scales[i], zeros[i], b[i]))
