@@ -460,6 +460,18 @@ int w8_test_bounded_wait(uint64_t limit_ns, void *stream);
  */
 int w8_test_set_decode_helper_delay(uint64_t delay_ns);
 
+/*
+ * w8_test_w8a8_cluster_stall -- test hook for w8a8_linear's cluster kernel: a
+ * w8a8_linear call without zeros and bias, by that kernel with tiles of 128
+ * tokens, in which the second block of every cluster receives no operands and
+ * every wait lasts 2 ms at most.  The waits run out, the status word says so,
+ * and no output is stored.  W8_ERR_SHAPE where the shape has no clusters (too
+ * many output tiles for the GPU, or K <= 448).
+ */
+int w8_test_w8a8_cluster_stall(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums,
+                               const uint8_t *packed, const uint16_t *scales, uint16_t *Y, int64_t M, int64_t K,
+                               int64_t N, void *stream);
+
 /* w8_version -- ABI version of this header (major * 100 + minor). */
 int w8_version(void);
 

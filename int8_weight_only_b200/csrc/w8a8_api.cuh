@@ -162,7 +162,7 @@ int w8a8_cluster_size(DeviceInfo *d, int64_t units, int64_t KB) {
     return 0;
 }
 
-template <int TN>
+template <int TN, bool kStall = false>
 int launch_w8a8_cluster(int c, int64_t units, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p,
                         cudaStream_t st) {
     CUtensorMap map;
@@ -182,7 +182,7 @@ int launch_w8a8_cluster(int c, int64_t units, const int8_t *q, int64_t ldq, int6
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, w8a8::cluster::w8a8_cluster_kernel<TN>, map, p) != cudaSuccess) return cuda_fail();
+    if (cudaLaunchKernelEx(&cfg, w8a8::cluster::w8a8_cluster_kernel<TN, kStall>, map, p) != cudaSuccess) return cuda_fail();
     return launch_status();
 }
 
@@ -325,14 +325,15 @@ int launch_w8a8_grouped(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, 
 
 cudaError_t w8a8_attributes() {
     cudaError_t e = cudaSuccess;
-#define W8_I8_CLUSTER_SMEM(TN)                                                                            \
+#define W8_I8_CLUSTER_SMEM(TN, STALL)                                                                     \
     if (e == cudaSuccess)                                                                                     \
-        e = cudaFuncSetAttribute((const void *)w8a8::cluster::w8a8_cluster_kernel<TN>,                       \
+        e = cudaFuncSetAttribute((const void *)w8a8::cluster::w8a8_cluster_kernel<TN, STALL>,                \
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, w8a8::cluster::Cfg<TN>::kSmemBytes);
-    W8_I8_CLUSTER_SMEM(16)
-    W8_I8_CLUSTER_SMEM(32)
-    W8_I8_CLUSTER_SMEM(64)
-    W8_I8_CLUSTER_SMEM(128)
+    W8_I8_CLUSTER_SMEM(16, false)
+    W8_I8_CLUSTER_SMEM(32, false)
+    W8_I8_CLUSTER_SMEM(64, false)
+    W8_I8_CLUSTER_SMEM(128, false)
+    W8_I8_CLUSTER_SMEM(128, true)
 #undef W8_I8_CLUSTER_SMEM
 #define W8_I8_SMEM(TN)                                                                                        \
     if (e == cudaSuccess)                                                                                     \
@@ -360,11 +361,13 @@ cudaError_t w8a8_attributes() {
     return e;
 }
 
-// The linear of one weight (offsets == nullptr, groups == 1) or of one weight
-// per group.
+// The linear of one weight (offsets == nullptr, groups == 1), of one weight per
+// group, or of one weight with a block of each cluster stalled.
+enum class Form { kOne, kGrouped, kStalled };
 int w8a8_common(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums, const int32_t *offsets,
-                bool grouped, int64_t groups, const uint8_t *packed, const uint16_t *scales, const int8_t *zeros,
+                Form form, int64_t groups, const uint8_t *packed, const uint16_t *scales, const int8_t *zeros,
                 const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K, int64_t N, void *stream) {
+    const bool grouped = form == Form::kGrouped;
     if (M < 0 || K < 1 || N < 1 || K % 8 != 0 || N % 8 != 0 || K > kMaxSumK || M > (int64_t)INT32_MAX - 512 ||
         N > (1LL << 30) || ldq < K || ldq % 16 != 0 || ldq >= (1LL << 40))
         return W8_ERR_SHAPE;
@@ -399,6 +402,11 @@ int w8a8_common(const int8_t *q, int64_t ldq, const float *x_scales, const int32
     p.NB = (int)cdiv(N, 128);
     p.KB = (int)cdiv(K, 64);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (form == Form::kStalled) {
+        const int64_t units = cdiv(M, 128) * p.NB;
+        const int c = w8a8_cluster_size<128>(d, units, p.KB);
+        return c > 0 ? launch_w8a8_cluster<128, true>(c, units, q, ldq, K, p, st) : W8_ERR_SHAPE;
+    }
     return grouped ? launch_w8a8_grouped(d, q, ldq, K, p, st) : launch_w8a8(d, q, ldq, K, p, st);
 }
 
@@ -419,14 +427,21 @@ int w8_swiglu_quantize_per_token(const uint16_t *H, int64_t ldh, int64_t M, int6
 int w8a8_linear(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums, const uint8_t *packed,
                 const uint16_t *scales, const int8_t *zeros, const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K,
                 int64_t N, void *stream) {
-    return w8a8_common(q, ldq, x_scales, x_sums, nullptr, false, 1, packed, scales, zeros, bias, Y, M, K, N, stream);
+    return w8a8_common(q, ldq, x_scales, x_sums, nullptr, Form::kOne, 1, packed, scales, zeros, bias, Y, M, K, N, stream);
+}
+
+int w8_test_w8a8_cluster_stall(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums,
+                               const uint8_t *packed, const uint16_t *scales, uint16_t *Y, int64_t M, int64_t K,
+                               int64_t N, void *stream) {
+    return w8a8_common(q, ldq, x_scales, x_sums, nullptr, Form::kStalled, 1, packed, scales, nullptr, nullptr, Y, M, K, N,
+                       stream);
 }
 
 int w8a8_linear_grouped(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums,
                         const int32_t *offsets, int64_t groups, const uint8_t *packed, const uint16_t *scales,
                         const int8_t *zeros, const uint16_t *bias, uint16_t *Y, int64_t M, int64_t K, int64_t N,
                         void *stream) {
-    return w8a8_common(q, ldq, x_scales, x_sums, offsets, true, groups, packed, scales, zeros, bias, Y, M, K, N,
+    return w8a8_common(q, ldq, x_scales, x_sums, offsets, Form::kGrouped, groups, packed, scales, zeros, bias, Y, M, K, N,
                        stream);
 }
 

@@ -34,18 +34,23 @@ struct Cfg {
     static_assert(kSmemBytes <= 227 * 1024 - 2048, "shared memory budget");
 };
 
-// grid = output tiles x C blocks in clusters of C (2, 4 or 8).
-template <int TN>
+// A block whose waits run out sends no sums: the count of every block that
+// should have had them stays short, so no block of the cluster stores.
+
+// grid = output tiles x C blocks in clusters of C (2, 4 or 8).  kStall, for the
+// tests: the second block of each cluster copies nothing, and waits last 2 ms.
+template <int TN, bool kStall = false>
 __global__ void __launch_bounds__(Cfg<TN>::kThreads, 1)
 w8a8_cluster_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ Params p) {
     using C = Cfg<TN>;
+    constexpr unsigned long long kLimitNs = kStall ? 2000000ull : kWaitLimitNs;
     constexpr int kEpi = 32 * C::kEpiWarps;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *gather = ring + C::kStages * C::kStageBytes;
     __shared__ uint64_t full[C::kStages], empty[C::kStages];
-    __shared__ uint64_t d_full, gathered;
+    __shared__ uint64_t d_full, drain, gathered;
     __shared__ uint32_t tmem_base_sh;
     __shared__ __align__(16) int sum_sh[TN];
     __shared__ __align__(16) float xs_sh[TN];
@@ -69,6 +74,7 @@ w8a8_cluster_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_con
             mbar_init(&empty[i], 1);
         }
         mbar_init(&d_full, 1);
+        mbar_init(&drain, 1);
         mbar_init(&gathered, 1);
         mbar_arrive_expect_tx(&gathered, (uint32_t)((csz - 1) * width * n16 * 4));
         fence_barrier_init();
@@ -94,9 +100,9 @@ w8a8_cluster_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_con
             pdl_wait();
             int st = 0, issued = 0;
             uint32_t ph = 0;
-            for (int kb = kb0; kb < kb1; kb += C::kStep) {
+            for (int kb = kStall && rank == 1 ? kb1 : kb0; kb < kb1; kb += C::kStep) {
                 const int cnt = min(C::kStep, kb1 - kb), boxes = (cnt + 1) >> 1;
-                if (!mbar_wait(&empty[st], ph ^ 1u, SITE_I8_EMPTY)) break;
+                if (!mbar_wait(&empty[st], ph ^ 1u, SITE_I8_EMPTY, kLimitNs)) break;
                 uint8_t *ws = ring + st * C::kStageBytes, *xs = ws + C::kWBytes;
                 mbar_arrive_expect_tx(&full[st], cnt * kTile + boxes * C::kXBox);
                 bulk_g2s(ws, w + (int64_t)(kb - kb0) * kTile, cnt * kTile, &full[st]);
@@ -116,12 +122,13 @@ w8a8_cluster_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_con
         pdl_wait();   // before the first bounded wait: its second is this call's own
         int st = 0;
         uint32_t ph = 0, acc = 0;
+        bool ok = true;
         const uint64_t w_desc0 = smem_desc_kmajor_sw64(smem_u32(ring));
         const uint64_t x_desc0 = smem_desc_kmajor_sw128(smem_u32(ring) + C::kWBytes);
         const uint32_t idesc = idesc_u8_s8_s32(kBN, n16);
         for (int kb = kb0; kb < kb1; kb += C::kStep) {
             const int cnt = min(C::kStep, kb1 - kb);
-            if (!warp_all(mbar_wait(&full[st], ph, SITE_I8_FULL))) break;
+            if (!warp_all(mbar_wait(&full[st], ph, SITE_I8_FULL, kLimitNs))) { ok = false; break; }
             tc_fence_after();
             const uint64_t wd = w_desc0 + (uint32_t)st * (C::kStageBytes / 16);
             const uint64_t xd = x_desc0 + (uint32_t)st * (C::kStageBytes / 16);
@@ -140,10 +147,12 @@ w8a8_cluster_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_con
             acc = 1;
             if (++st == C::kStages) { st = 0; ph ^= 1u; }
         }
-        // every product is complete before the tensor memory is read or freed
-        if (elect_one()) tc_commit(&d_full);
+        // every product is complete before the tensor memory is read or freed;
+        // sums that miss some are not passed on
+        uint64_t *const done = ok ? &d_full : &drain;
+        if (elect_one()) tc_commit(done);
         __syncwarp();
-        mbar_wait(&d_full, 0, SITE_I8_DRAIN);
+        mbar_wait(done, 0, SITE_I8_DRAIN);
     } else if (warp >= 4) {
         // ---------------------------------------------------- gather, scale and store
         pdl_wait();
@@ -162,14 +171,15 @@ w8a8_cluster_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_con
             sum_sh[t] = t < nr ? __ldg(p.x_sums + row0 + t) : 0;
             xs_sh[t] = t < nr ? __ldg(p.x_scales + row0 + t) : 0.0f;
         }
-        const bool ok = warp_all(mbar_wait(&d_full, 0, SITE_I8_DFULL));
+        const bool ok = warp_all(mbar_wait(&d_full, 0, SITE_I8_DFULL, kLimitNs));
         tc_fence_after();
         // [source block][token quad][channel of the receiver][4]
         const int quads = TN / 4;
         const int to = r / width;
         const uint32_t slot = (uint32_t)((rank * quads * width + r % width) * 16);
         const uint32_t dst = mapa_shared(smem_u32(gather), to) + slot, bar = mapa_shared(smem_u32(&gathered), to);
-        for (int c0 = cb; c0 < min(n16, cb + C::kEpiTokens); c0 += 16) {
+        const int c_end = ok ? min(n16, cb + C::kEpiTokens) : cb;
+        for (int c0 = cb; c0 < c_end; c0 += 16) {
             uint32_t v[16];
             tmem_load_16(tmem + ((uint32_t)(32 * q4) << 16) + c0, v);
 #pragma unroll
@@ -183,7 +193,10 @@ w8a8_cluster_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_con
             }
         }
         named_bar_sync(1, kEpi);   // this block's own sums, the tokens' sums and scales
-        if (named_bar_all(1, kEpi, ok && mbar_wait_cluster(&gathered, 0, SITE_I8_DRAIN))) {
+        // (a block without sums of its own waits as well: the others' are on
+        // their way into its shared memory)
+        const bool all = mbar_wait_cluster(&gathered, 0, SITE_I8_DRAIN, kLimitNs);
+        if (named_bar_all(1, kEpi, ok && all)) {
             uint16_t *const y = p.Y + row0 * p.N + n;
             for (int qd = tid / width; 4 * qd < nr; qd += kEpi / width) {
                 int4 s = make_int4(0, 0, 0, 0);

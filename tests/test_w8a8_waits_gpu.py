@@ -1,5 +1,5 @@
 """The bounded waits of the W8A8 kernels: their second begins when the kernel
-before has ended."""
+before has ended, and one that runs out leaves the outputs as they were."""
 import pytest
 
 from tests.gpu_helpers import to_gpu, to_np, w8
@@ -41,3 +41,39 @@ def test_a_long_kernel_before_does_not_use_up_the_wait(M, K, N, E):
         r = slice(at[e], at[e + 1]) if E else slice(0, M)
         i = e if E else ()
         assert_linear(first[r], *linear(q[r], xs[r], w[i], scales[i], zeros[i], b[i]))
+
+
+# clusters of 8, 4 and 2 blocks; the last with two token tiles
+@pytest.mark.parametrize("M,K,N", [(3, 4096, 256), (100, 1024, 1032), (20, 512, 4096), (150, 2048, 1024)])
+def test_a_cluster_that_gives_up_stores_nothing(M, K, N):
+    import torch
+    m = w8()
+    lib = m.load_library()
+    q, xs, sums, w, scales, _, _ = operands(M, K, N, M + N)
+    a = [pitched(torch, q), to_gpu(xs), to_gpu(sums), m.prepack(to_gpu(w)), to_gpu(scales)]
+    out = torch.full((M, N), 3.5, dtype=torch.float16, device="cuda")
+    assert m.device_status() == 0
+    m._call(lib.w8_test_w8a8_cluster_stall, "w8_test_w8a8_cluster_stall", out.device, m._raw_stream(out.device),
+            a[0].data_ptr(), a[0].stride(0), *[t.data_ptr() for t in a[1:]], out.data_ptr(), M, K, N)
+    status = m.device_status()
+    assert status & 1 and 0x60 <= (status >> 8) & 0xFF <= 0x64
+    assert bool((out == 3.5).all())
+    # the GPU and the next call are as before
+    got = to_np(m.linear_w8a8(*a, out=out))
+    assert_linear(got, *linear(q, xs, w, scales))
+    assert m.device_status() == 0
+
+
+def test_the_stalled_form_needs_clusters():
+    import torch
+    m = w8()
+    lib = m.load_library()
+    for M, K, N in ((3, 448, 256), (3, 4096, 27392)):
+        q, xs, sums = torch.zeros((M, K), dtype=torch.int8, device="cuda"), torch.zeros(M, device="cuda"), torch.zeros(M, dtype=torch.int32, device="cuda")
+        packed = torch.zeros(m.prepacked_bytes(K, N), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(N, dtype=torch.float16, device="cuda")
+        out = torch.empty((M, N), dtype=torch.float16, device="cuda")
+        with pytest.raises(m.W8Error):
+            m._call(lib.w8_test_w8a8_cluster_stall, "w8_test_w8a8_cluster_stall", out.device, m._raw_stream(out.device),
+                    q.data_ptr(), K, xs.data_ptr(), sums.data_ptr(), packed.data_ptr(), scales.data_ptr(), out.data_ptr(),
+                    M, K, N)
