@@ -472,6 +472,14 @@ int w8_test_w8a8_cluster_stall(const int8_t *q, int64_t ldq, const float *x_scal
                                const uint8_t *packed, const uint16_t *scales, uint16_t *Y, int64_t M, int64_t K,
                                int64_t N, void *stream);
 
+/*
+ * w8_test_w8a8_kernel -- test hook: the kernel that w8a8_linear (groups == 0)
+ * or w8a8_linear_grouped takes for these sizes on the current device, as 1000
+ * kind + tokens of a tile; kind 1: whole tiles on single SMs, 2: clusters, 3:
+ * pairs of SMs.  Negative: W8_ERR_SHAPE, W8_ERR_DEVICE or W8_ERR_CUDA.
+ */
+int w8_test_w8a8_kernel(int64_t M, int64_t K, int64_t N, int64_t groups);
+
 /* w8_version -- ABI version of this header (major * 100 + minor). */
 int w8_version(void);
 

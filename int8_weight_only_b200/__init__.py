@@ -93,6 +93,7 @@ def load_library():
         lib.w8a8_linear.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp]
         lib.w8a8_linear_grouped.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, vp]
         lib.w8_test_w8a8_cluster_stall.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, vp]
+        lib.w8_test_w8a8_kernel.argtypes = [i64, i64, i64, i64]
         lib.w8_error_string.argtypes = [i32]
         lib.w8_error_string.restype = ctypes.c_char_p
         lib.w8_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
@@ -101,7 +102,7 @@ def load_library():
         lib.w8_version.argtypes = []
         for f in ("w8_quantize_per_channel", "w8_prepack", "w8_unpack", "w8a16_linear",
                   "w8a16_linear_decode_static", "w8_quantize_per_token", "w8_swiglu_quantize_per_token",
-                  "w8a8_linear", "w8a8_linear_grouped", "w8_test_w8a8_cluster_stall",
+                  "w8a8_linear", "w8a8_linear_grouped", "w8_test_w8a8_cluster_stall", "w8_test_w8a8_kernel",
                   "w8_device_status", "w8_test_bounded_wait", "w8_test_set_decode_helper_delay",
                   "w8_version"):
             getattr(lib, f).restype = i32

@@ -186,10 +186,10 @@ int launch_w8a8_cluster(int c, int64_t units, const int8_t *q, int64_t ldq, int6
     return launch_status();
 }
 
+// One weight on single SMs: clusters of c blocks, or (c == 0) whole tiles.
 template <int TN>
-int launch_w8a8_as(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
+int launch_w8a8_as(DeviceInfo *d, int c, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
     const int64_t units = cdiv(p.rows, TN) * p.NB;
-    const int c = w8a8_cluster_size<TN>(d, units, p.KB);
     if (c > 0) return launch_w8a8_cluster<TN>(c, units, q, ldq, K, p, st);
     CUtensorMap map;
     const int rc = make_map_codes(&map, q, ldq, p.rows, K, TN);
@@ -262,6 +262,13 @@ int launch_w8a8_pair(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, con
     return launch_status();
 }
 
+enum class Kernel { kTiles = 1, kCluster = 2, kPair = 3 };
+struct Choice {
+    Kernel kernel;
+    int tokens;    // of a tile
+    int cluster;   // blocks of a cluster, of kCluster
+};
+
 // The kernel of a product of one weight.  Up to 128 tokens: one token tile,
 // split over K (w8a8.cuh, w8a8_cluster.cuh).  Above, whichever of three ways
 // is shortest by a line through measured times, in microseconds: a tile's K
@@ -270,20 +277,34 @@ int launch_w8a8_pair(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, con
 // call 4.9, 4.2 and 3.9 besides.  Measured / by the line: 512 x 4096 x 4096
 // 14.1 / 15.1, 12.0 / 11.9, 18.8 / 14.8; 512 x 8016 x 1312 21.8 / 25.1, 18.3 /
 // 19.3, 15.0 / 14.6; 2048 x 8016 x 1312 24.0 / 25.1, 33.2 / 34.4, 31.7 / 46.7.
+Choice choose_w8a8(DeviceInfo *d, int64_t M, int64_t NB, int64_t KB) {
+    const int tn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int64_t units = cdiv(M, tn) * NB;
+    const int c = tn == 16   ? w8a8_cluster_size<16>(d, units, KB)
+                  : tn == 32 ? w8a8_cluster_size<32>(d, units, KB)
+                  : tn == 64 ? w8a8_cluster_size<64>(d, units, KB)
+                             : w8a8_cluster_size<128>(d, units, KB);
+    if (M > 128) {
+        const int64_t pairs = std::max(1, d->sms / 2), steps = cdiv(KB, 2);
+        const double t256 = 4.9 + 0.32 * (double)(cdiv(cdiv(M, 256) * cdiv(NB, 2), pairs) * steps);
+        const double t128 = 4.2 + 0.24 * (double)(cdiv(cdiv(M, 128) * cdiv(NB, 2), pairs) * steps);
+        const double one = 3.9 + 0.17 * (double)(c > 0 ? cdiv(KB, c) : cdiv(units, d->sms) * KB);
+        if (one >= t128 || one >= t256) return {Kernel::kPair, t128 < t256 ? 128 : 256, 0};
+    }
+    return {c > 0 ? Kernel::kCluster : Kernel::kTiles, tn, c};
+}
+
 int launch_w8a8(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
-    const int64_t M = p.rows;
-    if (M <= 16) return launch_w8a8_as<16>(d, q, ldq, K, p, st);
-    if (M <= 32) return launch_w8a8_as<32>(d, q, ldq, K, p, st);
-    if (M <= 64) return launch_w8a8_as<64>(d, q, ldq, K, p, st);
-    if (M <= 128) return launch_w8a8_as<128>(d, q, ldq, K, p, st);
-    const int64_t pairs = std::max(1, d->sms / 2), steps = cdiv(p.KB, 2), units = cdiv(M, 128) * p.NB;
-    const double t256 = 4.9 + 0.32 * (double)(cdiv(cdiv(M, 256) * cdiv(p.NB, 2), pairs) * steps);
-    const double t128 = 4.2 + 0.24 * (double)(cdiv(cdiv(M, 128) * cdiv(p.NB, 2), pairs) * steps);
-    const int c = w8a8_cluster_size<128>(d, units, p.KB);
-    const double one = 3.9 + 0.17 * (double)(c > 0 ? cdiv(p.KB, c) : cdiv(units, d->sms) * p.KB);
-    if (one < t128 && one < t256) return launch_w8a8_as<128>(d, q, ldq, K, p, st);
-    if (t128 < t256) return launch_w8a8_pair<128, false>(d, q, ldq, K, p, st);
-    return launch_w8a8_pair<256, false>(d, q, ldq, K, p, st);
+    const Choice c = choose_w8a8(d, p.rows, p.NB, p.KB);
+    if (c.kernel == Kernel::kPair)
+        return c.tokens == 128 ? launch_w8a8_pair<128, false>(d, q, ldq, K, p, st)
+                               : launch_w8a8_pair<256, false>(d, q, ldq, K, p, st);
+    switch (c.tokens) {
+        case 16: return launch_w8a8_as<16>(d, c.cluster, q, ldq, K, p, st);
+        case 32: return launch_w8a8_as<32>(d, c.cluster, q, ldq, K, p, st);
+        case 64: return launch_w8a8_as<64>(d, c.cluster, q, ldq, K, p, st);
+        default: return launch_w8a8_as<128>(d, c.cluster, q, ldq, K, p, st);
+    }
 }
 
 // Groups on single SMs (w8a8.cuh): one block each, the kernel deals the tiles.
@@ -316,11 +337,18 @@ int launch_w8a8_groups(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, c
 // 24.0 / -, 16 25.6 / 23.7, 24.3 / 25.9, 64 54.6 / 37.2, 25.7 / 27.6, 128 - / -,
 // 31.2 / 30.2, 256 - / -, 46.0 / 40.0; 39 groups of 288 x 11040, 23 tokens each:
 // 53.4 / 50.7, 33.0 / 33.2.
+Choice choose_w8a8_grouped(int64_t M, int64_t groups, int64_t K) {
+    if (M <= 4 * groups) return {Kernel::kTiles, 16, 0};
+    if (M <= 16 * groups && K >= 1024) return {Kernel::kTiles, 32, 0};
+    return {Kernel::kPair, M > 96 * groups ? 256 : 128, 0};
+}
+
 int launch_w8a8_grouped(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
-    if (p.rows <= 4 * (int64_t)p.groups) return launch_w8a8_groups<16>(d, q, ldq, K, p, st);
-    if (p.rows <= 16 * (int64_t)p.groups && K >= 1024) return launch_w8a8_groups<32>(d, q, ldq, K, p, st);
-    if (p.rows > 96 * (int64_t)p.groups) return launch_w8a8_pair<256, true>(d, q, ldq, K, p, st);
-    return launch_w8a8_pair<128, true>(d, q, ldq, K, p, st);
+    const Choice c = choose_w8a8_grouped(p.rows, p.groups, K);
+    if (c.kernel == Kernel::kTiles)
+        return c.tokens == 16 ? launch_w8a8_groups<16>(d, q, ldq, K, p, st) : launch_w8a8_groups<32>(d, q, ldq, K, p, st);
+    return c.tokens == 128 ? launch_w8a8_pair<128, true>(d, q, ldq, K, p, st)
+                           : launch_w8a8_pair<256, true>(d, q, ldq, K, p, st);
 }
 
 cudaError_t w8a8_attributes() {
@@ -443,6 +471,17 @@ int w8a8_linear_grouped(const int8_t *q, int64_t ldq, const float *x_scales, con
                         void *stream) {
     return w8a8_common(q, ldq, x_scales, x_sums, offsets, Form::kGrouped, groups, packed, scales, zeros, bias, Y, M, K, N,
                        stream);
+}
+
+int w8_test_w8a8_kernel(int64_t M, int64_t K, int64_t N, int64_t groups) {
+    if (M < 1 || M > (int64_t)INT32_MAX - 512 || K < 1 || K > kMaxSumK || N < 1 || N > (1LL << 30) || groups < 0 ||
+        groups > w8a8::kMaxGroups)
+        return W8_ERR_SHAPE;
+    DeviceInfo *d = nullptr;
+    const int rc = device_info(&d);
+    if (rc != W8_OK) return rc;
+    const Choice c = groups > 0 ? choose_w8a8_grouped(M, groups, K) : choose_w8a8(d, M, cdiv(N, 128), cdiv(K, 64));
+    return 1000 * (int)c.kernel + c.tokens;
 }
 
 }  // extern "C"
