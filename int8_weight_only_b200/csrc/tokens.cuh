@@ -101,18 +101,20 @@ __device__ __forceinline__ void swiglu8(const uint4 &g, const uint4 &u, uint64_t
 }
 
 // Eight consecutive values of a row, from element k (of the SwiGLU with the
-// sign turned).
+// sign turned).  By ordinary loads: the kernel before, which may still run when
+// this one begins, writes X, and the read-only path (ld.global.nc) is for memory
+// that nobody writes in the meantime.
 template <int kSrc>
 __device__ __forceinline__ void load8(const Params &p, int64_t row, int64_t k, uint64_t (&f)[4]) {
     if constexpr (kSrc == kF32) {
         const ulonglong2 *src = reinterpret_cast<const ulonglong2 *>(static_cast<const float *>(p.X) + row * p.ldx + k);
-        const ulonglong2 a = __ldg(src), b = __ldg(src + 1);
+        const ulonglong2 a = src[0], b = src[1];
         f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
     } else if constexpr (kSrc == kF16) {
-        widen8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.X) + row * p.ldx + k)), f);
+        widen8(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.X) + row * p.ldx + k), f);
     } else {
         const uint16_t *src = static_cast<const uint16_t *>(p.X) + row * p.ldx + k;
-        const uint4 g = __ldg(reinterpret_cast<const uint4 *>(src)), u = __ldg(reinterpret_cast<const uint4 *>(src + p.K));
+        const uint4 g = *reinterpret_cast<const uint4 *>(src), u = *reinterpret_cast<const uint4 *>(src + p.K);
         swiglu8(g, u, f);
     }
 }
@@ -254,8 +256,8 @@ __global__ void __launch_bounds__(kBlock<TPR>, kFirst && TPR == 256 && V >= 5 &&
 #pragma unroll
             for (int c = 0; c < V; ++c) {
                 if (k0 + c * kStep < p.K) {
-                    g[c] = __ldg(reinterpret_cast<const uint4 *>(src + c * kStep));
-                    u[c] = __ldg(reinterpret_cast<const uint4 *>(src + p.K + c * kStep));
+                    g[c] = *reinterpret_cast<const uint4 *>(src + c * kStep);
+                    u[c] = *reinterpret_cast<const uint4 *>(src + p.K + c * kStep);
                 }
             }
 #pragma unroll

@@ -352,8 +352,8 @@ w8a8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
             // the tokens' sums and scales, read while the products run; the
             // other buffer may still be read for the tile before
             if (const int c = threadIdx.x - 128; c < TN) {
-                sum_sh[d][c] = c < nr ? __ldg(p.x_sums + row0 + c) : 0;
-                xs_sh[d][c] = c < nr ? __ldg(p.x_scales + row0 + c) : 0.0f;
+                sum_sh[d][c] = c < nr ? p.x_sums[row0 + c] : 0;
+                xs_sh[d][c] = c < nr ? p.x_scales[row0 + c] : 0.0f;
             }
             uint16_t *const y0 = p.Y + row0 * p.N + n;
             auto store = [&](const uint32_t (&v)[kChunk], int c0) {

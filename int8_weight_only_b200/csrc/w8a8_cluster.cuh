@@ -168,8 +168,8 @@ w8a8_cluster_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_con
         const float bi = (n_ok && p.bias) ? __half2float(__ushort_as_half(p.bias[n])) : 0.0f;
         const int off = 128 + ((n_ok && p.zeros) ? (int)p.zeros[n] : 0);
         for (int t = tid; t < TN; t += kEpi) {
-            sum_sh[t] = t < nr ? __ldg(p.x_sums + row0 + t) : 0;
-            xs_sh[t] = t < nr ? __ldg(p.x_scales + row0 + t) : 0.0f;
+            sum_sh[t] = t < nr ? p.x_sums[row0 + t] : 0;
+            xs_sh[t] = t < nr ? p.x_scales[row0 + t] : 0.0f;
         }
         const bool ok = warp_all(mbar_wait(&d_full, 0, SITE_I8_DFULL, kLimitNs));
         tc_fence_after();

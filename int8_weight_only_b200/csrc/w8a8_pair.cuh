@@ -295,8 +295,8 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
                 o.bi[j] = ok && p.bias ? p.bias[at + 8 * j] : (uint16_t)0;
                 o.z[j] = ok && p.zeros ? p.zeros[at + 8 * j] : (int8_t)0;
             }
-            o.sum = c_own < o.nr ? __ldg(p.x_sums + o.row0 + c_own) : 0;
-            o.xs = c_own < o.nr ? __ldg(p.x_scales + o.row0 + c_own) : 0.0f;
+            o.sum = c_own < o.nr ? p.x_sums[o.row0 + c_own] : 0;
+            o.xs = c_own < o.nr ? p.x_scales[o.row0 + c_own] : 0.0f;
             return true;
         };
         Operands next;
