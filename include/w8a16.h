@@ -344,11 +344,11 @@ int w8_swiglu_quantize_per_token(const uint16_t *H, int64_t ldh, int64_t M, int6
  *   stay below 2^31 whatever the codes are); N >= 1 with N % 8 == 0.
  *   No workspace: the call keeps nothing in memory of its own, so calls on
  *   different streams and captured graphs may overlap.
- * Kernel choice (internal): up to 128 tokens, and beyond where the product is
- *   small, output tiles of 128 channels on single SMs, one cluster of 2 to 8
- *   thread blocks for each (split over K, the sums gathered in distributed
- *   shared memory) where the tiles are few; else pairs of SMs with tiles of
- *   256 channels x 128 or 256 tokens.  All run the 8-bit integer tcgen05
+ * Kernel choice (internal, by lines through measured times): up to 128 tokens,
+ *   and beyond where the product is small, output tiles of 128 channels on
+ *   single SMs, one cluster of 2 to 8 thread blocks for each (split over K, the
+ *   sums gathered in distributed shared memory) where the tiles are few and K is
+ *   long; else pairs of SMs with tiles of 256 channels x 256 tokens.  All run the 8-bit integer tcgen05
  *   product on the packed weight as it stands.
  * Results: the integer sum is exact and independent of how the work is split;
  *   fp32 rounds it, the product with s_m and the fused product with s_n plus
@@ -466,7 +466,7 @@ int w8_test_set_decode_helper_delay(uint64_t delay_ns);
  * tokens, in which the second block of every cluster receives no operands and
  * every wait lasts 2 ms at most.  The waits run out, the status word says so,
  * and no output is stored.  W8_ERR_SHAPE where the shape has no clusters (too
- * many output tiles for the GPU, or K <= 448).
+ * many output tiles for the GPU, or K <= 192).
  */
 int w8_test_w8a8_cluster_stall(const int8_t *q, int64_t ldq, const float *x_scales, const int32_t *x_sums,
                                const uint8_t *packed, const uint16_t *scales, uint16_t *Y, int64_t M, int64_t K,

@@ -10,16 +10,17 @@
 //   sum_k x (w - z) = sum_k x u - (128 + z) sum_k x
 // and sum_k x, one integer per token, comes with the activations.
 //
-// This kernel: few tokens, whole output tiles of 128 channels x TN tokens dealt
-// round robin to the thread blocks.  It is bound by the weight stream (1 x 4096
+// This kernel: whole output tiles of 128 channels x TN tokens dealt round robin
+// to the thread blocks, for few tokens and for products of about one wave of
+// tiles (512 x 4096 x 4096: 10.4 us, on pairs of SMs 14.4).  With one token it is bound by the weight stream (1 x 4096
 // x 27392: 18.4 us, 6.1 TB/s, 93 % of the measured copy rate), which
 // 94 of 148 SMs already draw at 5.7 TB/s, so sharing output tiles to occupy
 // all SMs does not pay: an even split over K, the parts added through the
-// workspace, took 21.7 us against 20.0 for 1 x 4096 x 27392 (107 blocks with
-// two tiles each), 14.7 against 12.0 for 1 x 4096 x 13696 and 31.4 against 29.0
-// for 1 x 13696 x 12000.  Fewer than half as many output tiles as SMs go to
-// clusters (w8a8_cluster.cuh).  Groups of few tokens (kGrouped) run here too,
-// their tiles counted on the device (8 groups of 2 x 4096 x 4096: 21.3 us).
+// workspace, took 21.7 us for 1 x 4096 x 27392 (107 blocks with two tiles each),
+// and against a first form of whole tiles 14.7 to 12.0 for 1 x 4096 x 13696 and
+// 31.4 to 29.0 for 1 x 13696 x 12000.  Few output tiles with a long K go to clusters
+// (w8a8_cluster.cuh).  Groups of few tokens (kGrouped) run here too,
+// their tiles counted on the device (8 groups of 2 x 4096 x 4096: 22 us).
 //
 // Roles: warp 0 producer (weight tiles by one bulk copy, tokens by TMA),
 // warp 1 issues the products, warp 2 owns the tensor memory, warps 4 and up

@@ -125,41 +125,34 @@ int make_map_codes(CUtensorMap *map, const int8_t *q, int64_t ldq, int64_t rows,
     return r == CUDA_SUCCESS ? W8_OK : W8_ERR_CUDA;
 }
 
-// Blocks of a cluster for few output tiles (w8a8_cluster.cuh), 0 where the
-// even split over all blocks serves better: the largest C whose clusters can
-// all run at once, with at least kClusterRun weight tiles for each block
-// (1 x 1024 x 1024: 2.9 us with 4, 3.2 with 8, 4.2 with 16; 100 x 1024 x 1024:
-// 5.0, 5.8, 5.7).
-constexpr int64_t kClusterRun = 4;
+// Whether `units` clusters of c blocks (w8a8_cluster.cuh) can all run at once,
+// with two weight tiles at least for each block.
 template <int TN>
-int w8a8_cluster_size(DeviceInfo *d, int64_t units, int64_t KB) {
-    for (int c = w8a8::cluster::kMaxCluster; c >= 2; c >>= 1) {
-        if (units * c > d->sms || KB < (int64_t)c * kClusterRun) continue;
-        const void *fn = (const void *)w8a8::cluster::w8a8_cluster_kernel<TN>;
-        std::lock_guard<std::mutex> lock(g_mu);
-        int &cached = d->dclusters[{fn, c}];
-        if (cached == 0) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)(d->sms / c * c), 1, 1);
-            cfg.blockDim = dim3(w8a8::cluster::Cfg<TN>::kThreads, 1, 1);
-            cfg.dynamicSmemBytes = w8a8::cluster::Cfg<TN>::kSmemBytes;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = c;
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, w8a8::cluster::w8a8_cluster_kernel<TN>, &cfg) != cudaSuccess) {
-                cudaGetLastError();
-                n = 0;
-            }
-            cached = n > 0 ? n : -1;
+bool w8a8_cluster_fits(DeviceInfo *d, int c, int64_t units, int64_t KB) {
+    if (units * c > d->sms || KB < 2 * c) return false;
+    const void *fn = (const void *)w8a8::cluster::w8a8_cluster_kernel<TN>;
+    std::lock_guard<std::mutex> lock(g_mu);
+    int &cached = d->dclusters[{fn, c}];
+    if (cached == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(d->sms / c * c), 1, 1);
+        cfg.blockDim = dim3(w8a8::cluster::Cfg<TN>::kThreads, 1, 1);
+        cfg.dynamicSmemBytes = w8a8::cluster::Cfg<TN>::kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = c;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, w8a8::cluster::w8a8_cluster_kernel<TN>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
         }
-        if (cached >= units) return c;
+        cached = n > 0 ? n : -1;
     }
-    return 0;
+    return cached >= units;
 }
 
 template <int TN, bool kStall = false>
@@ -269,36 +262,59 @@ struct Choice {
     int cluster;   // blocks of a cluster, of kCluster
 };
 
-// The kernel of a product of one weight.  Up to 128 tokens: one token tile,
-// split over K (w8a8.cuh, w8a8_cluster.cuh).  Above, whichever of three ways
-// is shortest by a line through measured times, in microseconds: a tile's K
-// steps of 128 features take 0.32 (256 tokens a tile, pairs of SMs) or 0.24
-// (128 tokens), a weight tile of 64 features 0.17 (128 tokens, one SM), and a
-// call 4.9, 4.2 and 3.9 besides.  Measured / by the line: 512 x 4096 x 4096
-// 14.1 / 15.1, 12.0 / 11.9, 18.8 / 14.8; 512 x 8016 x 1312 21.8 / 25.1, 18.3 /
-// 19.3, 15.0 / 14.6; 2048 x 8016 x 1312 24.0 / 25.1, 33.2 / 34.4, 31.7 / 46.7.
+// The kernel of a product of one weight: whichever is shortest by a line through
+// its measured times, in microseconds.
+//   whole tiles on single SMs (w8a8.cuh):  a + waves (e + b weight tiles of K)
+//   clusters (w8a8_cluster.cuh):           a + e blocks + b weight tiles a block
+//   pairs of SMs (w8a8_pair.cuh):          a + waves (e + b steps of 128 features)
+// with tiles of 16, 32, 64 or 128 tokens on single SMs and of 256 on pairs, for
+// more than 128 tokens.  Over 1052 sizes of 1 to 4096 tokens, each measured with
+// every kernel that takes it, the choice is 0.9 % above the best in the mean, 1.27
+// times it at worst (16 x 256 x 256, 2.8 against 2.2).  Measured and (by the line):
+//                        tiles        clusters of 2   of 4        pairs
+//   16 x 512 x 9216      2.8 (2.8)    4.1 (4.3)
+//   1 x 4096 x 4096      7.8 (7.6)    6.0 (6.0)       6.1 (5.3)
+//   512 x 768 x 2304     4.4 (4.9)    7.0 (7.3)                   6.3 (6.1)
+//   512 x 4096 x 4096    10.4 (10.4)                              14.4 (13.5)
+//   1024 x 4096 x 4096   17.8 (18.9)                              15.1 (13.5)
+// Pairs with tiles of 128 tokens (512 x 768 x 2304 5.1, 512 x 4096 x 4096 12.0)
+// would be 5 % or more ahead of the choice for 39 of 484 sizes above 128 tokens,
+// but no line tells which: with them in it the choice was 0.03 % better in the
+// mean.  Groups take them.
+struct Line {
+    double a, e, b;
+};
+constexpr Line kTileLine[4] = {{1.1, 1.05, 0.0845}, {1.1, 1.4, 0.0845}, {1.1, 1.75, 0.0845}, {2.0, 1.6, 0.107}};
+constexpr Line kClusterLine[4] = {{2.25, 0.012, 0.092}, {2.75, 0.013, 0.092}, {3.1, 0.014, 0.10}, {4.5, 0.013, 0.155}};
+constexpr Line kPairLine = {2.65, 1.75, 0.284};
+
 Choice choose_w8a8(DeviceInfo *d, int64_t M, int64_t NB, int64_t KB) {
-    const int tn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int i = M <= 16 ? 0 : M <= 32 ? 1 : M <= 64 ? 2 : 3, tn = 16 << i;
     const int64_t units = cdiv(M, tn) * NB;
-    const int c = tn == 16   ? w8a8_cluster_size<16>(d, units, KB)
-                  : tn == 32 ? w8a8_cluster_size<32>(d, units, KB)
-                  : tn == 64 ? w8a8_cluster_size<64>(d, units, KB)
-                             : w8a8_cluster_size<128>(d, units, KB);
-    if (M > 128) {
-        const int64_t pairs = std::max(1, d->sms / 2), steps = cdiv(KB, 2);
-        const double t256 = 4.9 + 0.32 * (double)(cdiv(cdiv(M, 256) * cdiv(NB, 2), pairs) * steps);
-        const double t128 = 4.2 + 0.24 * (double)(cdiv(cdiv(M, 128) * cdiv(NB, 2), pairs) * steps);
-        const double one = 3.9 + 0.17 * (double)(c > 0 ? cdiv(KB, c) : cdiv(units, d->sms) * KB);
-        if (one >= t128 || one >= t256) return {Kernel::kPair, t128 < t256 ? 128 : 256, 0};
+    Choice best = {Kernel::kTiles, tn, 0};
+    double least = kTileLine[i].a + (double)cdiv(units, d->sms) * (kTileLine[i].e + kTileLine[i].b * (double)KB);
+    for (int c = w8a8::cluster::kMaxCluster; c >= 2; c >>= 1) {
+        const double t = kClusterLine[i].a + kClusterLine[i].e * (double)(units * c) + kClusterLine[i].b * (double)cdiv(KB, c);
+        if (t >= least) continue;
+        const bool fits = i == 0   ? w8a8_cluster_fits<16>(d, c, units, KB)
+                          : i == 1 ? w8a8_cluster_fits<32>(d, c, units, KB)
+                          : i == 2 ? w8a8_cluster_fits<64>(d, c, units, KB)
+                                   : w8a8_cluster_fits<128>(d, c, units, KB);
+        if (fits) {
+            least = t;
+            best = {Kernel::kCluster, tn, c};
+        }
     }
-    return {c > 0 ? Kernel::kCluster : Kernel::kTiles, tn, c};
+    if (M > 128) {
+        const int64_t waves = cdiv(cdiv(M, 256) * cdiv(NB, 2), std::max(1, d->sms / 2));
+        if (kPairLine.a + (double)waves * (kPairLine.e + kPairLine.b * (double)cdiv(KB, 2)) < least) best = {Kernel::kPair, 256, 0};
+    }
+    return best;
 }
 
 int launch_w8a8(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, const w8a8::Params &p, cudaStream_t st) {
     const Choice c = choose_w8a8(d, p.rows, p.NB, p.KB);
-    if (c.kernel == Kernel::kPair)
-        return c.tokens == 128 ? launch_w8a8_pair<128, false>(d, q, ldq, K, p, st)
-                               : launch_w8a8_pair<256, false>(d, q, ldq, K, p, st);
+    if (c.kernel == Kernel::kPair) return launch_w8a8_pair<256, false>(d, q, ldq, K, p, st);
     switch (c.tokens) {
         case 16: return launch_w8a8_as<16>(d, c.cluster, q, ldq, K, p, st);
         case 32: return launch_w8a8_as<32>(d, c.cluster, q, ldq, K, p, st);
@@ -378,13 +394,13 @@ cudaError_t w8a8_attributes() {
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute((const void *)w8a8::w8a8_kernel<32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  w8a8::Cfg<32>::kSmemBytes);
-#define W8_I8_PAIR_SMEM(BT)                                                                                   \
-    for (const void *f : {(const void *)w8a8::pair::w8a8_pair_kernel<BT, false>,                             \
-                          (const void *)w8a8::pair::w8a8_pair_kernel<BT, true>})                              \
-        if (e == cudaSuccess)                                                                                 \
-            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, w8a8::pair::Cfg<BT>::kSmemBytes);
-    W8_I8_PAIR_SMEM(128)
-    W8_I8_PAIR_SMEM(256)
+#define W8_I8_PAIR_SMEM(BT, GROUPED)                                                                          \
+    if (e == cudaSuccess)                                                                                     \
+        e = cudaFuncSetAttribute((const void *)w8a8::pair::w8a8_pair_kernel<BT, GROUPED>,                    \
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, w8a8::pair::Cfg<BT>::kSmemBytes);
+    W8_I8_PAIR_SMEM(256, false)
+    W8_I8_PAIR_SMEM(128, true)
+    W8_I8_PAIR_SMEM(256, true)
 #undef W8_I8_PAIR_SMEM
     return e;
 }
@@ -432,8 +448,9 @@ int w8a8_common(const int8_t *q, int64_t ldq, const float *x_scales, const int32
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (form == Form::kStalled) {
         const int64_t units = cdiv(M, 128) * p.NB;
-        const int c = w8a8_cluster_size<128>(d, units, p.KB);
-        return c > 0 ? launch_w8a8_cluster<128, true>(c, units, q, ldq, K, p, st) : W8_ERR_SHAPE;
+        for (int c = w8a8::cluster::kMaxCluster; c >= 2; c >>= 1)
+            if (w8a8_cluster_fits<128>(d, c, units, p.KB)) return launch_w8a8_cluster<128, true>(c, units, q, ldq, K, p, st);
+        return W8_ERR_SHAPE;
     }
     return grouped ? launch_w8a8_grouped(d, q, ldq, K, p, st) : launch_w8a8(d, q, ldq, K, p, st);
 }

@@ -4,10 +4,13 @@
 // integer sums of channels [128 k / C, 128 (k + 1) / C) from all C blocks in
 // its shared memory, by asynchronous distributed-shared-memory stores counted
 // on its barrier, adds, scales and stores them: no workspace, no counter, no
-// fence, and every block finishes a share of the tile.  Bound by the weight
-// stream and, when that is short, by one start, one gather and one store: 1 x
-// 4096 x 4096 4.9 us (8.8 with the parts added through the workspace), 128 x
-// 4096 x 4096 8.2 (16.1), 48 x 13696 x 4096 13.1 (17.2; 4.3 TB/s).
+// fence, and every block finishes a share of the tile.  Bound by what one SM
+// takes in, and when that is short by one start, one gather and one store: a
+// block loads all tokens of the tile for its share of K beside its weights, 602
+// KB an SM of which 164 are tokens for 48 x 13696 x 4096, at 56 KB a microsecond
+// (SMs that stream weights alone take 61).  1 x 4096 x 4096 5.0 us (8.8 with the
+// parts added through a workspace), 128 x 4096 x 4096 8.3 (16.1), 48 x 13696 x
+// 4096 13.0 (17.2).
 #pragma once
 
 #include "w8a8.cuh"

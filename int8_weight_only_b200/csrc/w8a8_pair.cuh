@@ -1,6 +1,6 @@
 // W8A8 linear for many tokens, on pairs of SMs (tcgen05 cta_group::2): the
 // product of w8a8.cuh with output tiles of 256 channels x BT tokens (256, or
-// 128 where tiles of 256 would not fill the GPU).  Each block of a cluster of
+// 128 for groups of few).  Each block of a cluster of
 // two holds its own 128 channels of the weight and half of the tile's tokens
 // in shared memory, so a 128-wide K step of a 256 x 256 tile brings 32 KB into
 // each SM for 512 cycles of integer products; the 32-bit sums of two tiles fit

@@ -10,9 +10,9 @@ pytestmark = pytest.mark.gpu
 LONG_NS = 1_300_000_000     # more than a wait's one second
 
 
-# (M, K, N, groups): clusters of 8 and of 2, whole tiles on single SMs, pairs
-# of SMs with tiles of 128 and of 256 tokens, and the groups' three kernels
-@pytest.mark.parametrize("M,K,N,E", [(3, 4096, 256, 0), (100, 1024, 1024, 0), (5, 256, 16384, 0), (140, 1032, 4968, 0),
+# (M, K, N, groups): clusters, whole tiles on single SMs with few and many
+# tokens, pairs of SMs, and the groups' kernels
+@pytest.mark.parametrize("M,K,N,E", [(3, 4096, 256, 0), (100, 4096, 1024, 0), (5, 256, 16384, 0), (140, 1032, 4968, 0),
                                      (520, 1032, 4968, 0), (6, 1024, 264, 3), (40, 1024, 264, 2), (300, 520, 264, 2)])
 def test_a_long_kernel_before_does_not_use_up_the_wait(M, K, N, E):
     import torch
@@ -68,7 +68,7 @@ def test_the_stalled_form_needs_clusters():
     import torch
     m = w8()
     lib = m.load_library()
-    for M, K, N in ((3, 448, 256), (3, 4096, 27392)):
+    for M, K, N in ((3, 192, 256), (3, 4096, 27392)):
         q, xs, sums = torch.zeros((M, K), dtype=torch.int8, device="cuda"), torch.zeros(M, device="cuda"), torch.zeros(M, dtype=torch.int32, device="cuda")
         packed = torch.zeros(m.prepacked_bytes(K, N), dtype=torch.uint8, device="cuda")
         scales = torch.zeros(N, dtype=torch.float16, device="cuda")
