@@ -334,7 +334,9 @@ int w8_swiglu_quantize_per_token(const uint16_t *H, int64_t ldh, int64_t M, int6
  *   q         [M, K] int8 activation codes, rows ldq >= K bytes apart (ldq a
  *             multiple of 16), with x_scales [M] fp32 and x_sums [M] int32
  *             (the sum of each row's K codes), as w8_quantize_per_token
- *             writes them.  Codes made elsewhere may be any int8 values.
+ *             writes them.  Codes made elsewhere may be any int8 values.  All
+ *             three on 16-byte boundaries, as every pointer here: x_scales + r
+ *             for r % 4 == 0 only.
  *   packed    w8_prepack output for the [K, N] weight (symmetric or
  *             asymmetric codes).
  *   scales    [N] fp16;  zeros  [N] int8 zero points, or NULL for none;

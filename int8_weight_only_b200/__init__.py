@@ -606,7 +606,9 @@ def _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, lead):
 def linear_w8a8(q, x_scales, x_sums, packed, scales, bias=None, zeros=None, out=None):
     """Y [M, N] fp16 = x_scales scales (q . (w - zeros)) (+ bias) for the
     output of quantize_tokens (or of swiglu_quantize_tokens) and a packed
-    weight; zeros for codes from quantize_asym."""
+    weight; zeros for codes from quantize_asym.  Every tensor has to start on a
+    16-byte boundary: of the tokens from r on, x_scales[r:] and x_sums[r:] do
+    where r % 4 == 0, elsewhere they need a clone()."""
     lib = load_library()
     ldq, M, K, N, out = _w8a8_operands(q, x_scales, x_sums, packed, scales, bias, zeros, out, ())
     dev = q.device

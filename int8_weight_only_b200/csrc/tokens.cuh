@@ -13,8 +13,10 @@
 // One pass over X: a row is spread over TPR threads, each of which holds its
 // values in registers between the row maximum and the rounding, so the plain
 // quantizer is bound by HBM for many rows (4096 x 4096 fp32: 13.6 us, 6.2 TB/s)
-// and by latency for few (1 x 4096: 1.6 us).  The SwiGLU is bound by the issue
-// of instructions, 28 a value (2048 x 13696: 40.7 us, 3.4 TB/s).
+// and by latency for few (1 x 4096: 1.6 us).  The SwiGLU (2048 x 13696: 40.9 us,
+// 3.4 TB/s) saturates nothing: 28 instructions a value keep the schedulers busy
+// in 56 % of the cycles, and three blocks an SM, each of loads, arithmetic,
+// barrier and codes, do not cover one another's phases.
 #pragma once
 
 #include "i8.cuh"
@@ -233,7 +235,10 @@ constexpr int kBlock = TPR == 32 ? 256 : TPR;
 // x 13696: 47.2 -> 40.8) and not where its registers cost a wave of blocks (512
 // x 13696: 12.6 -> 15.1; the plain quantizer, 4096 x 13696 fp16: 35.8 -> 45.7).
 // Rows brought ahead into shared memory by a producer thread were no faster
-// (2048 x 13696: 44.6): the issue of instructions, 29 a value, is the bound.
+// (2048 x 13696: 44.6).  Of kFirst with 256 threads three blocks share an SM up to
+// V = 7, where the compiler by itself takes registers for two (2048 rows of 10240:
+// 26.7 us with the bound, 33.1 without; 12288: 31.3, 38.6; 13696, with 24 bytes of
+// spills: 40.8, 42.9); V = 8 would spill more than that gives (16384: 50.4, 50.1).
 template <int kSrc, int TPR, int V, bool kFirst>
 __global__ void __launch_bounds__(kBlock<TPR>, kFirst && TPR == 256 && V >= 5 && V <= 7 ? 3 : 0) quantize_tokens_kernel(const __grid_constant__ Params p) {
     __shared__ float sh_max[TPR / 32];

@@ -12,15 +12,15 @@
 //
 // This kernel: whole output tiles of 128 channels x TN tokens dealt round robin
 // to the thread blocks, for few tokens and for products of about one wave of
-// tiles (512 x 4096 x 4096: 10.4 us, on pairs of SMs 14.4).  With one token it is bound by the weight stream (1 x 4096
-// x 27392: 18.4 us, 6.1 TB/s, 93 % of the measured copy rate), which
-// 94 of 148 SMs already draw at 5.7 TB/s, so sharing output tiles to occupy
-// all SMs does not pay: an even split over K, the parts added through the
-// workspace, took 21.7 us for 1 x 4096 x 27392 (107 blocks with two tiles each),
-// and against a first form of whole tiles 14.7 to 12.0 for 1 x 4096 x 13696 and
-// 31.4 to 29.0 for 1 x 13696 x 12000.  Few output tiles with a long K go to clusters
-// (w8a8_cluster.cuh).  Groups of few tokens (kGrouped) run here too,
-// their tiles counted on the device (8 groups of 2 x 4096 x 4096: 22 us).
+// tiles (512 x 4096 x 4096: 10.4 us, on pairs of SMs 14.4).  With few tokens it
+// is bound by the weight stream (1 x 4096 x 27392: 18.3 us, 6.1 TB/s, 94 % of the
+// measured copy rate), which 94 of 148 SMs already draw at 5.7 TB/s, so sharing
+// output tiles to occupy all SMs does not pay: an even split over K, the parts
+// added through a workspace, took 21.7 us for 1 x 4096 x 27392 (107 blocks with
+// two tiles each), and against a first form of whole tiles 14.7 to 12.0 for 1 x
+// 4096 x 13696 and 31.4 to 29.0 for 1 x 13696 x 12000.  Few output tiles with a
+// long K go to clusters (w8a8_cluster.cuh).  Groups of few tokens (kGrouped) run
+// here too, their tiles counted on the device (8 groups of 2 x 4096 x 4096: 22 us).
 //
 // Roles: warp 0 producer (weight tiles by one bulk copy, tokens by TMA),
 // warp 1 issues the products, warp 2 owns the tensor memory, warps 4 and up

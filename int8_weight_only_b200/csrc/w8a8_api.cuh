@@ -352,7 +352,9 @@ int launch_w8a8_groups(DeviceInfo *d, const int8_t *q, int64_t ldq, int64_t K, c
 // groups of 4096 x 4096: 2 tokens each 21.3 / 21.7, 23.5 / -, 8 23.0 / 23.4,
 // 24.0 / -, 16 25.6 / 23.7, 24.3 / 25.9, 64 54.6 / 37.2, 25.7 / 27.6, 128 - / -,
 // 31.2 / 30.2, 256 - / -, 46.0 / 40.0; 39 groups of 288 x 11040, 23 tokens each:
-// 53.4 / 50.7, 33.0 / 33.2.
+// 53.4 / 50.7, 33.0 / 33.2.  How the rows spread the host cannot see: with all of
+// them in one group the mean misleads most (128 rows in one of 8 groups of 4096 x
+// 13696, taken with tiles of 32: 23.6, where tiles of 128 on pairs take 14.2).
 Choice choose_w8a8_grouped(int64_t M, int64_t groups, int64_t K) {
     if (M <= 4 * groups) return {Kernel::kTiles, 16, 0};
     if (M <= 16 * groups && K >= 1024) return {Kernel::kTiles, 32, 0};
