@@ -444,8 +444,9 @@ int w8_device_status(void *stream, uint32_t *out);
  * limit in nanoseconds (1e3 .. 5e9); the wait gives up, records site 0xEE in
  * the device status word and the kernel returns.  Used by the tests to
  * check that a wait that runs out ends the kernel cleanly.  The next kernel of
- * the stream may be launched as soon as this one has started, as behind every
- * kernel of this library; its own waits begin when this one has ended.
+ * the stream may be launched as soon as this one has started, as behind most
+ * kernels of this library; the waits of the W8A8 linears begin when this one has
+ * ended.
  */
 int w8_test_bounded_wait(uint64_t limit_ns, void *stream);
 
